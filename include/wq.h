@@ -21,7 +21,7 @@
  *   - An empty problem (n_vec == 0, rows == 0) returns WQ_OK and enqueues nothing; its pointers
  *     may then be NULL.
  *   - Element types: WQ_F32 = IEEE binary32, WQ_BF16 = bfloat16 (raw 16-bit patterns).
- *   - Unless an entry point states otherwise (tq3_encode, rpbh_linear, tq3_attention reorder the
+ *   - Unless an entry point states otherwise (tq3_encode, tq3_cache_append, rpbh_linear and the attention calls reorder the
  *     arithmetic and say how), all arithmetic is fp32 in the order the pages give, except the two
  *     L2 norms, whose squares are summed in fp64 and rounded once to fp32 after the square root.
  */
@@ -176,6 +176,50 @@ wq_status tq3_attention_paged(const void *q, int q_dtype, int64_t heads, int64_t
                               int64_t pages_per_head, int64_t page_size, int64_t S, const uint32_t *sign_mask,
                               float softmax_scale, void *out, int out_dtype, void *stream);
 
+/* --------------------------------------------------------------------------------------------
+ * The cache of a batch of sequences. K and V are pools [n_pages][kv_heads][page_size] of 56-byte
+ * records (the record of tq3_encode_aos), page_size a power of two, 1 .. 2^30, kv_heads 1 .. 65535.
+ * One page table per sequence, page_table[b][0 .. pages_per_seq-1] (int32), serves all heads and both
+ * pools: token j of sequence b is place j % page_size of page page_table[b][j / page_size]. Seen by
+ * tq3_decode_paged and tq3_attention_paged, (page, head) is page number page * kv_heads + head.
+ * Entries that no token needs are not read. No counterpart on the page beyond the record.
+ * -------------------------------------------------------------------------------------------- */
+
+/* tq3_cache_append -- tq3_quantize of the K and the V of new tokens, written to their slots: token t
+ * of head h goes to place slots[t] % page_size of page slots[t] / page_size, in both pools.
+ * norm = max(||x||, 1e-8), scale = max(max|y|, 1e-8), idx_i = #{j : B_j < y_i / scale} with
+ * y = H (s . x) / (sqrt(128) norm). Precision: the indices are those of real arithmetic (a vector with
+ * a coefficient near a boundary is decided in fp64), so they do not depend on the order of the sums;
+ * tq3_encode and tq3_encode_exact may differ from them by one step where y_i / scale is within 1e-6 of
+ * a boundary. Norms agree with their real values to within 1e-6 relative, scales to within 6e-6 (the
+ * bound; about 1e-7 in practice). A norm beyond the fp32 range is stored as +inf, with every index 3, as the page's division by it gives.
+ *   k, v       device, tokens x kv_heads rows of 128 elements of dtype, 16-byte aligned. Strides are in
+ *              elements, not negative, and multiples of 16 bytes: a slice of a fused projection will do.
+ *   slots      device, tokens x int64, 8-byte aligned. A negative slot skips the token (padding); a slot
+ *              at or beyond n_pages * page_size is skipped and sets device fault bit 6. Where two tokens
+ *              have the same slot, the records there are unspecified afterwards.
+ *   k_pool, v_pool  device, 16-byte aligned; records that no slot names are untouched.
+ * Errors: WQ_ERR_SHAPE (negative counts or strides, kv_heads or page_size out of range),
+ * WQ_ERR_DTYPE, WQ_ERR_NULL, WQ_ERR_ALIGN, WQ_ERR_CUDA. tokens == 0 enqueues nothing. */
+wq_status tq3_cache_append(const void *k, const void *v, int dtype, int64_t tokens, int64_t kv_heads,
+                           int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                           int64_t v_head_stride, const uint32_t *sign_mask, const int64_t *slots,
+                           uint8_t *k_pool, uint8_t *v_pool, int64_t n_pages, int64_t page_size, void *stream);
+
+/* tq3_cache_read -- tq3_dequantize of ragged sequences: rows seq_start[b] .. seq_start[b+1]-1 of k_out
+ * and v_out receive tokens 0, 1, .. of sequence b, decoded as tq3_decode does (the same bits).
+ *   seq_start  device, (batch + 1) x int32, ascending, 4-byte aligned. Rows before seq_start[0] and from
+ *              seq_start[batch] on are left as they were.
+ *   n_tokens   rows of k_out and v_out, below 2^31.
+ *   k_out, v_out  device, [n_tokens][kv_heads][128] of out_dtype, 16-byte aligned.
+ * A token beyond pages_per_seq pages, or whose entry is negative or not below n_pages, decodes as zeros
+ * and sets device fault bit 6.
+ * Errors: as tq3_cache_append. n_tokens == 0 or batch == 0 enqueues nothing. */
+wq_status tq3_cache_read(const uint8_t *k_pool, const uint8_t *v_pool, int64_t n_pages, int64_t kv_heads,
+                         int64_t page_size, const int32_t *page_table, int64_t batch, int64_t pages_per_seq,
+                         const int32_t *seq_start, int64_t n_tokens, const uint32_t *sign_mask, void *k_out,
+                         void *v_out, int out_dtype, void *stream);
+
 /* tq3_compressed_bytes -- tq3_memory_bytes' compressed size for n_vec vectors: 56 * n_vec
  * (-1 if n_vec < 0 or the product overflows). */
 int64_t tq3_compressed_bytes(int64_t n_vec);
@@ -307,8 +351,8 @@ wq_status wq_rpbh_codebook(int bits, int64_t d, float *out);
  * leaving its outputs unspecified: bit 0 a TQ3 kernel waiting for a TMA tile, bit 1 an RPBH kernel
  * waiting for a row copy or the CUDA-core attention waiting for a tile's records, bit 3 the tensor-core TQ3 encoder waiting for a tile or its product,
  * bit 4 rpbh_linear waiting for a tile, the unpacked weights or its product, bit 5 the self-test
- * wq_selftest_wait_timeout, bit 7 the tensor-core attention waiting for its product. Bit 6 is not a wait: tq3_encode_slots, tq3_decode_paged or
- * tq3_attention_paged met a slot or page-table entry outside the pool (that record was skipped,
+ * wq_selftest_wait_timeout, bit 7 the tensor-core attention waiting for its product. Bit 6 is not a wait: a call that takes slots or a page table
+ * met a slot or page-table entry outside the pool (that record was skipped,
  * decoded as zeros, or masked out of the attention; the rest of the call is complete).
  * Synchronous (a device-to-host copy on the legacy default stream); `flags` is host memory.
  * Errors: WQ_ERR_NULL, WQ_ERR_CUDA. */

@@ -436,6 +436,9 @@ unsigned int tq3_attn_read_and_clear_fault();  // tq3_attn.cu
 namespace rpbh_lanes {
 unsigned int read_and_clear_fault();  // rpbh_lanes.cu
 }
+namespace tq3_cache {
+unsigned int read_and_clear_fault();  // tq3_cache.cu
+}
 }
 
 extern "C" wq_status wq_device_fault(unsigned int *flags) {
@@ -449,7 +452,8 @@ extern "C" wq_status wq_device_fault(unsigned int *flags) {
     const unsigned int l = rpbh_linear::read_and_clear_fault();
     const unsigned int a = tq3_attn_read_and_clear_fault();
     const unsigned int n = rpbh_lanes::read_and_clear_fault();
-    if ((r | q | t | l | a | n) & 0x80000000u) return WQ_ERR_CUDA;
-    *flags = v | r | q | t | l | a | n;
+    const unsigned int c = tq3_cache::read_and_clear_fault();
+    if ((r | q | t | l | a | n | c) & 0x80000000u) return WQ_ERR_CUDA;
+    *flags = v | r | q | t | l | a | n | c;
     return WQ_OK;
 }

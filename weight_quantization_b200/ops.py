@@ -32,6 +32,9 @@ PROTOTYPES = {
     "tq3_attention": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _i64, _vp, C.c_float, _vp, _int, _vp]),
     "tq3_attention_paged": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp, C.c_float,
                                    _vp, _int, _vp]),
+    "tq3_cache_append": (_int, [_vp, _vp, _int, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64,
+                                _vp]),
+    "tq3_cache_read": (_int, [_vp, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _int, _vp]),
     "tq3_compressed_bytes": (_i64, [_i64]),
     "rpbh_quantize_weight": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _int, _vp, _vp, _vp, _vp]),
     "rpbh_requantize_weight": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _int, _vp, _vp, _vp, _int, _vp]),
@@ -311,6 +314,107 @@ def tq3_attention_paged(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
                                    _dev(out, "out"), _DT[out.dtype], _stream(q.device))
     _check("tq3_attention_paged", st)
     return out
+
+
+def _rows128(t, name: str):
+    """[tokens, heads, 128] rows that may be a slice of a wider tensor: the last axis dense, the other
+    strides multiples of 16 bytes. Returns (pointer, token stride, head stride) in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DT:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    if t.ndim != 3 or t.shape[2] != 128:
+        raise ValueError(f"{name} must be [tokens, heads, 128]")
+    # the stride of an axis of one element is never used
+    token = t.stride(0) if t.shape[0] > 1 else 0
+    head = t.stride(1) if t.shape[1] > 1 else 0
+    if t.numel() and (t.stride(2) != 1 or token * t.element_size() % 16 or head * t.element_size() % 16
+                      or t.data_ptr() % 16):
+        raise ValueError(f"{name} must have dense rows that start on multiples of 16 bytes")
+    return t.data_ptr(), token, head
+
+
+def _cache_pools(k_pool, v_pool, device):
+    """Checks the pools of a batch's cache; returns (n_pages, kv_heads, page_size)."""
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        _on(t, device, name, (torch.uint8,))
+        if t.ndim != 4 or t.shape[3] != 56:
+            raise ValueError(f"{name} must be uint8 [n_pages, kv_heads, page_size, 56]")
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} must start on a multiple of 16 bytes")
+    if k_pool.shape != v_pool.shape:
+        raise ValueError("k_pool and v_pool must have the same shape")
+    return k_pool.shape[:3]
+
+
+def _cache_table(page_table, device):
+    _on(page_table, device, "page_table", (torch.int32,))
+    if page_table.ndim != 2:
+        raise ValueError("page_table must be int32 [batch, pages_per_seq]")
+    return page_table.shape
+
+
+def tq3_cache_append(k: torch.Tensor, v: torch.Tensor, sign_mask, slots: torch.Tensor, k_pool: torch.Tensor,
+                     v_pool: torch.Tensor):
+    """TQ3-encode the K and V of new tokens into a batch's paged cache: k, v [tokens, kv_heads, 128]
+    (fp32/bf16; slices of a fused projection will do), pools uint8 [n_pages, kv_heads, page_size, 56].
+    Token t goes to place slots[t] % page_size of page slots[t] // page_size (int64; a negative slot
+    skips the token, one outside the pool is skipped and raises device fault bit 6; slots are distinct).
+    Indices near a boundary are decided in fp64. Returns (k_pool, v_pool)."""
+    kp, k_token, k_head = _rows128(k, "k")
+    vp, v_token, v_head = _rows128(v, "v")
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have the same shape and dtype")
+    _on(v, k.device, "v")
+    n_pages, heads, page_size = _cache_pools(k_pool, v_pool, k.device)
+    if k.shape[1] != heads:
+        raise ValueError("k and v must have the pools' heads")
+    _on(slots, k.device, "slots", (torch.int64,))
+    if slots.numel() != k.shape[0]:
+        raise ValueError("slots must be int64 with one entry per token")
+    m = _mask_arg(sign_mask)
+    with torch.cuda.device(k.device):
+        st = lib().tq3_cache_append(kp, vp, _DT[k.dtype], k.shape[0], heads, k_token, k_head, v_token, v_head,
+                                    m.ctypes.data, _dev(slots, "slots"), _dev(k_pool, "k_pool"),
+                                    _dev(v_pool, "v_pool"), n_pages, page_size, _stream(k.device))
+    _check("tq3_cache_append", st)
+    return k_pool, v_pool
+
+
+def tq3_cache_read(k_pool: torch.Tensor, v_pool: torch.Tensor, page_table: torch.Tensor, seq_start: torch.Tensor,
+                   sign_mask, n_tokens: int, out_dtype=torch.bfloat16, k_out=None, v_out=None):
+    """Decode ragged sequences of a batch's paged cache to dense K and V [n_tokens, kv_heads, 128]
+    (fp32/bf16): rows seq_start[b] .. seq_start[b + 1] - 1 (int32 [batch + 1], ascending) are tokens
+    0, 1, .. of sequence b, read through page_table int32 [batch, pages_per_seq]. Rows of no sequence
+    are left as they were. Tokens without a page in the pool decode as zeros and raise device fault
+    bit 6. Returns (k_out, v_out)."""
+    if not isinstance(k_pool, torch.Tensor) or not k_pool.is_cuda:
+        raise ValueError("k_pool must be a CUDA tensor")
+    device = k_pool.device
+    n_pages, heads, page_size = _cache_pools(k_pool, v_pool, device)
+    batch, pages_per_seq = _cache_table(page_table, device)
+    _on(seq_start, device, "seq_start", (torch.int32,))
+    if seq_start.numel() != batch + 1:
+        raise ValueError("seq_start must be int32 [batch + 1]")
+    if n_tokens < 0:
+        raise ValueError("n_tokens must not be negative")
+    if k_out is None:
+        k_out = torch.empty((n_tokens, heads, 128), dtype=out_dtype, device=device)
+    if v_out is None:
+        v_out = torch.empty((n_tokens, heads, 128), dtype=k_out.dtype, device=device)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _on(t, device, name, (torch.float32, torch.bfloat16))
+        _fits(t, n_tokens * heads * 128, name)
+    if k_out.dtype != v_out.dtype:
+        raise ValueError("k_out and v_out must have the same dtype")
+    m = _mask_arg(sign_mask)
+    with torch.cuda.device(device):
+        st = lib().tq3_cache_read(_dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"), n_pages, heads, page_size,
+                                  _dev(page_table, "page_table"), batch, pages_per_seq, _dev(seq_start, "seq_start"),
+                                  n_tokens, m.ctypes.data, _dev(k_out, "k_out"), _dev(v_out, "v_out"),
+                                  _DT[k_out.dtype], _stream(device))
+    _check("tq3_cache_read", st)
+    return k_out, v_out
 
 
 def tq3_compressed_bytes(n_vec: int) -> int:
