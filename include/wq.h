@@ -220,6 +220,46 @@ wq_status tq3_cache_read(const uint8_t *k_pool, const uint8_t *v_pool, int64_t n
                          const int32_t *seq_start, int64_t n_tokens, const uint32_t *sign_mask, void *k_out,
                          void *v_out, int out_dtype, void *stream);
 
+/* tq3_attention_chunk -- causal attention of ragged chunks of new tokens over a batch's cache (which
+ * already holds the new tokens' K and V). Rows q_start[b] .. q_start[b+1]-1 of q are the n_q last tokens
+ * of sequence b, which has kv_len[b] keys: token i is at position p = kv_len[b] - n_q + i and sees the
+ * keys j <= p with, where window > 0, j > p - window or j < sinks. For each query head h,
+ *   out[token][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(softmax_scale * q[token][h] . k_j - max),
+ * over the keys that it sees, k_j and v_j the tq3_dequantize of the records of KV head
+ * h / (q_heads / kv_heads). A token that sees no key gets zeros. Rows of no sequence are left as they were.
+ *   q          device, n_tokens x q_heads rows of 128 elements of q_dtype, 16-byte aligned. Strides are in
+ *              elements, not negative, and multiples of 16 bytes: a slice of a fused projection will do.
+ *   q_heads    a multiple of kv_heads; n_tokens * q_heads / kv_heads < 2^31 - 4096.
+ *   page_table device, [batch][pages_per_seq] int32. Only entries of keys that some row sees are read,
+ *              so pages that a window has left behind may be freed. A key whose entry is negative or not
+ *              below n_pages is masked out and sets device fault bit 6, and so does a kv_len beyond
+ *              pages_per_seq * page_size (which then counts as that many keys).
+ *   q_start, kv_len  device, (batch + 1) and batch x int32, 4-byte aligned, q_start ascending.
+ *   max_q      how many new tokens a sequence has at most, to choose kernels and the workspace by; a
+ *              sequence with more is served all the same.
+ *   window     0: none. sinks: first keys that a window leaves visible.
+ *   out        device, [n_tokens][q_heads][128] of out_dtype, 16-byte aligned.
+ *   workspace  device, 16-byte aligned, tq3_attention_chunk_workspace(max_q, q_heads / kv_heads) bytes,
+ *              contents unspecified before and after. Calls that may run at the same time need one each.
+ * Precision: a logit is within (2^-11 + 2^-15) softmax_scale |q| |k_j| and each term of the value sum
+ * within 2^-10 of its own where q and out are bf16 (a bf16 result is rounded by up to 2^-8); within
+ * 2^-17 softmax_scale |q| |k_j|, and fp32 sums, where either is fp32. Sums are fp32, in an order that
+ * depends on the lengths alone. Record norms and scales are taken to be what the encoders write: not
+ * negative, and a value vector shorter than 2^-100 may count as one of that length.
+ * Errors: WQ_ERR_SHAPE (counts, strides, window or sinks out of range, softmax_scale not finite,
+ * workspace too small), WQ_ERR_DTYPE, WQ_ERR_NULL, WQ_ERR_ALIGN, WQ_ERR_CUDA. n_tokens == 0 or
+ * batch == 0 enqueues nothing. */
+wq_status tq3_attention_chunk(const void *q, int q_dtype, int64_t n_tokens, int64_t q_heads,
+                              int64_t q_token_stride, int64_t q_head_stride, const uint8_t *k_pool,
+                              const uint8_t *v_pool, int64_t n_pages, int64_t kv_heads, int64_t page_size,
+                              const int32_t *page_table, int64_t batch, int64_t pages_per_seq,
+                              const int32_t *q_start, const int32_t *kv_len, int64_t max_q, int64_t window,
+                              int64_t sinks, const uint32_t *sign_mask, float softmax_scale, void *out,
+                              int out_dtype, void *workspace, int64_t workspace_bytes, void *stream);
+/* Bytes of that workspace for up to max_q new tokens a sequence and `group` query heads per KV head
+ * (-1 if max_q < 0 or group < 1). */
+int64_t tq3_attention_chunk_workspace(int64_t max_q, int64_t group);
+
 /* tq3_compressed_bytes -- tq3_memory_bytes' compressed size for n_vec vectors: 56 * n_vec
  * (-1 if n_vec < 0 or the product overflows). */
 int64_t tq3_compressed_bytes(int64_t n_vec);

@@ -439,6 +439,9 @@ unsigned int read_and_clear_fault();  // rpbh_lanes.cu
 namespace tq3_cache {
 unsigned int read_and_clear_fault();  // tq3_cache.cu
 }
+namespace tq3_chunk {
+unsigned int read_and_clear_fault();  // tq3_chunk.cu
+}
 }
 
 extern "C" wq_status wq_device_fault(unsigned int *flags) {
@@ -453,7 +456,8 @@ extern "C" wq_status wq_device_fault(unsigned int *flags) {
     const unsigned int a = tq3_attn_read_and_clear_fault();
     const unsigned int n = rpbh_lanes::read_and_clear_fault();
     const unsigned int c = tq3_cache::read_and_clear_fault();
-    if ((r | q | t | l | a | n | c) & 0x80000000u) return WQ_ERR_CUDA;
-    *flags = v | r | q | t | l | a | n | c;
+    const unsigned int h = tq3_chunk::read_and_clear_fault();
+    if ((r | q | t | l | a | n | c | h) & 0x80000000u) return WQ_ERR_CUDA;
+    *flags = v | r | q | t | l | a | n | c | h;
     return WQ_OK;
 }

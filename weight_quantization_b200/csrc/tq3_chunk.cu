@@ -1,0 +1,630 @@
+// Attention of ragged chunks of new tokens over a batch's paged TQ3 cache (page "tq3_core.py": the
+// cache is what tq3_quantize compresses and tq3_dequantize restores), causal, optionally with a
+// sliding window and first tokens that stay visible. How the work is cut and joined is in
+// tq3_chunk.cuh; this file has the entry point, the join, and the kernel for few rows.
+//
+// With q~ = H (s . q), f_j = norm_j scale_j of key j and g_j that of value j (post = 128^-1/2):
+//     logit_ij = softmax_scale post f_j (q~_i . c[idx_j]),
+//     out_i    = s . H(sum_j p_ij g_j c[idx'_j]) post / sum_j p_ij,   p_ij = exp(logit_ij - max_i),
+// so both products are over centroids alone: 8 values, looked up as pairs (6 bits) in a table that
+// every lane has a column of in shared memory (a bank of its own, so no conflict).
+//
+// The rows kernel: a warp takes 16 keys at a time and one to NT times 8 rows of one KV head.
+// S^T = C_K q~^T and O^T += C_V^T w with m16n8k16: the looked-up pairs are the A operands as they are
+// (the 128 coordinates may be summed in any order, so a lane takes the coordinates whose bits it can
+// read as whole words), and no decoded key or value ever leaves the registers. In log2 units the
+// weights are taken as w_ij = 2^(s_ij + log2 g_j - M_i), which folds the value's factor into the
+// exponent, keeps w within fp16's range whatever the norms are, and leaves sum_j w_ij / g_j as the
+// softmax's denominator. M_i is raised only when it is passed by 2^8.
+//
+// Operands are fp16: the centroids times kGain are within 1.4e-5 of fp16 numbers, q~ is scaled by a
+// power of two per block of rows and rounded (2^-11 of each coordinate at most, so a logit moves by
+// 2^-11 softmax_scale |q| |k_j| at most), w likewise (2^-11 of a term). A bf16 result is rounded to 2^-8 afterwards. For
+// fp32 queries or results every operand is split into fp16 hi + lo (2^-22) and a product takes three
+// passes, hi hi + hi lo + lo hi. Sums are fp32.
+#include <cuda_runtime.h>
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "tq3_cache.cuh"
+#include "tq3_chunk.cuh"
+#include "tq3_common.cuh"
+
+namespace wq {
+namespace tq3_chunk {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kSub = kTileKeys / kWarps;  // keys of a warp's step
+static_assert(kSub == 16, "one m16n8k16 row block per step");
+constexpr int kStages = 4;
+constexpr int kStageBytes = 2 * kSub * tq3_cache::kRec;  // a step's key records, then its value records
+constexpr uint32_t kMaxPolls = 1u << 24;
+constexpr float kLazy = 8.0f;   // M_i is raised past this margin (log2 units)
+constexpr float kLift = 6.0f;   // weights are at most 2^(kLazy + kLift) < 65504, so 2^-20 of the largest is still normal
+constexpr float kTiny = 0x1p-100f;  // least g_j: a zero vector weighs 2^-100 instead
+
+__device__ unsigned int g_fault;
+
+// Shared memory of the rows kernel.
+template <int NT, bool kWide>
+struct Layout {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kTable = kWide ? 64 * 32 * 8 : 64 * 32 * 4;
+    static constexpr int kQ = kRows * 136;  // halves, rows padded by 16 bytes
+    static constexpr int kOffStage = kTable;
+    static constexpr int kOffQ = kOffStage + kWarps * kStages * kStageBytes;
+    static constexpr int kOffMerge = kOffQ + (kWide ? 2 : 1) * kQ * 2;
+    static constexpr int kOffStat = kOffMerge + kWarps * kRows * 132 * 4;  // per warp and row: M, l
+    static constexpr int kOffTop = kOffStat + kWarps * kRows * 8;          // per row: max |q~|
+    static constexpr int kOffBar = kOffTop + kRows * 4;
+    static constexpr int kOffValid = kOffBar + kWarps * kStages * 8;
+    static constexpr int kOffScratch = kOffValid + kWarps * kStages * 4;
+    static constexpr int kBytes = kOffScratch + (kWarps + 2) * 8;
+    static_assert(kOffMerge % 16 == 0 && kOffBar % 8 == 0 && kOffScratch % 8 == 0 && kBytes <= 227 * 1024, "layout");
+};
+
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// x - hi for the two halves of hi = pack_half2(a, b), as a pair again.
+__device__ __forceinline__ uint32_t residue_half2(float a, float b, uint32_t hi) {
+    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return pack_half2(__fsub_rn(a, h.x), __fsub_rn(b, h.y));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A pair of centroids: hi, and lo where the operands are split.
+template <bool kWide>
+struct Pair {
+    uint32_t hi, lo;
+};
+// The pair whose 6 bits are bits 7 .. 12 of x; `column` is this lane's column of the table.
+template <bool kWide>
+__device__ __forceinline__ Pair<kWide> lookup(const unsigned char *table, uint32_t column, uint32_t x) {
+    Pair<kWide> p;
+    if (kWide) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(table + (((x & 0x1f80u) << 1) | column));
+        p.hi = v.x, p.lo = v.y;
+    } else {
+        p.hi = *reinterpret_cast<const uint32_t *>(table + ((x & 0x1f80u) | column));
+        p.lo = 0;
+    }
+    return p;
+}
+// Bits o .. o + 5 of the words w, moved to bits 7 .. 12.
+template <int N>
+__device__ __forceinline__ uint32_t field(const uint32_t (&w)[N], int o) {
+    const int q = o >> 5, s = o & 31;
+    if (s < 7) return w[q] << (7 - s);
+    return s > 26 ? __funnelshift_r(w[q], w[q + 1 < N ? q + 1 : q], s - 7) : w[q] >> (s - 7);
+}
+
+template <int NT, bool kWide>
+__device__ __forceinline__ void product(float (&d)[4], const Pair<kWide> &a0, const Pair<kWide> &a1,
+                                        const Pair<kWide> &a2, const Pair<kWide> &a3, const uint32_t (&hi)[2],
+                                        const uint32_t (&lo)[2]) {
+    mma16816(d, a0.hi, a1.hi, a2.hi, a3.hi, hi[0], hi[1]);
+    if (kWide) {
+        mma16816(d, a0.lo, a1.lo, a2.lo, a3.lo, hi[0], hi[1]);
+        mma16816(d, a0.hi, a1.hi, a2.hi, a3.hi, lo[0], lo[1]);
+    }
+}
+
+// Whether the phase has completed, within the bounds of mbar_wait_bounded; the first poll is cheap.
+__device__ __forceinline__ bool wait_copy(uint64_t *bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(phase)
+                 : "memory");
+    return ok || mbar_wait_bounded(bar, phase, kMaxPolls);
+}
+
+// A warp's stream of 16-key steps through its stages.
+struct Steps {
+    unsigned char *stage;  // kStages of kStageBytes
+    uint64_t *bar;
+    uint32_t *valid;  // per stage: bit k = key k has a page
+    uint32_t issued, used;
+    bool dead;
+
+    // Requests the records of keys j0 .. j0 + 15 that some row sees (j <= last, and from <= j or
+    // j < until). page: the entry that holds all 16, where a page has 16 places or more.
+    __device__ __forceinline__ void issue(const Args &a, int b, int head, int j0, int last, int from, int until,
+                                          int32_t page, int lane) {
+        const int st = issued % kStages;
+        unsigned char *const dst = stage + st * kStageBytes;
+        const tq3_cache::Pools &pools = a.pools;
+        const int shift = pools.shift;
+        if (shift >= 4) {
+            const bool ok = page >= 0 && page < pools.n_pages;
+            if (lane == 0) {
+                valid[st] = ok ? 0xffffu : 0u;
+                if (ok) {
+                    const int64_t at = tq3_cache::record_at(pools, page, head, j0 & ((1 << shift) - 1));
+                    mbar_expect_tx(bar + st, kStageBytes);
+                    bulk_load(dst, pools.k + at, kStageBytes / 2, bar + st);
+                    bulk_load(dst + kStageBytes / 2, pools.v + at, kStageBytes / 2, bar + st);
+                } else {
+                    atomicOr(&g_fault, tq3::kFaultPoolIndex);
+                    mbar_arrive(bar + st);
+                }
+            }
+        } else {
+            // several pages, a lane each; a record alone is not a multiple of 16 bytes, so pages of one
+            // place are copied by the lanes themselves
+            const int size = 1 << shift, n = kSub >> shift;
+            const int k = lane & (n - 1), jp = j0 + (k << shift);
+            const bool mine = shift == 0 || lane < n;
+            const bool need = mine && jp <= last && (jp + size > from || jp < until);
+            const int32_t p = need ? __ldg(a.table + b * a.pages_per_seq + (jp >> shift)) : -1;
+            const bool ok = need && p >= 0 && p < pools.n_pages;
+            if (need && !ok) atomicOr(&g_fault, tq3::kFaultPoolIndex);
+            const uint32_t keys = __reduce_or_sync(0xffffffffu, ok ? ((1u << size) - 1u) << (k << shift) : 0u);
+            const int64_t at = ok ? tq3_cache::record_at(pools, p, head, 0) : 0;
+            if (lane == 0) valid[st] = keys;
+            if (shift == 0) {
+                uint2 r[7];
+                const uint8_t *const src = (lane < 16 ? pools.k : pools.v) + at;
+                uint2 *const to = reinterpret_cast<uint2 *>(dst + lane * tq3_cache::kRec);
+#pragma unroll
+                for (int i = 0; i < 7; ++i) r[i] = ok ? __ldg(reinterpret_cast<const uint2 *>(src) + i) : make_uint2(0u, 0u);
+#pragma unroll
+                for (int i = 0; i < 7; ++i) to[i] = r[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + st);
+            } else {
+                const uint32_t bytes = tq3_cache::kRec << shift;
+                if (lane == 0) mbar_expect_tx(bar + st, __popc(keys) * 2 * tq3_cache::kRec);
+                __syncwarp();
+                if (ok) {
+                    bulk_load(dst + k * bytes, pools.k + at, bytes, bar + st);
+                    bulk_load(dst + kStageBytes / 2 + k * bytes, pools.v + at, bytes, bar + st);
+                }
+            }
+        }
+        ++issued;
+    }
+    __device__ __forceinline__ bool arrived(int lane) {
+        const bool ok = __all_sync(0xffffffffu, wait_copy(bar + used % kStages, (used / kStages) & 1u));
+        if (!ok && lane == 0) atomicOr(&g_fault, 128u);
+        return ok;
+    }
+};
+
+template <int NT, bool kWide>
+__global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kernel(const __grid_constant__ Args a) {
+    using L = Layout<NT, kWide>;
+    constexpr int R = L::kRows;
+    // centroids times kGain: for one fp16 the gain at which all four magnitudes are nearest to fp16 numbers
+    constexpr float kGain = kWide ? 16.0f : 1.6196665f;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    unsigned char *const table = smem;
+    const uint32_t column = lane * (kWide ? 8 : 4);
+    __half *const qs = reinterpret_cast<__half *>(smem + L::kOffQ);
+    float *const merge = reinterpret_cast<float *>(smem + L::kOffMerge);
+    float *const stat = reinterpret_cast<float *>(smem + L::kOffStat);
+    float *const top = reinterpret_cast<float *>(smem + L::kOffTop);
+
+    for (int i = tid; i < 64 * 32; i += kThreads) {
+        const uint32_t f = i >> 5;
+        const float x = __fmul_rn(tq3::centroid(f & 7u), kGain), y = __fmul_rn(tq3::centroid(f >> 3), kGain);
+        const uint32_t hi = pack_half2(x, y);
+        if (kWide)
+            reinterpret_cast<uint2 *>(table)[i] = make_uint2(hi, residue_half2(x, y, hi));
+        else
+            reinterpret_cast<uint32_t *>(table)[i] = hi;
+    }
+    Steps steps;
+    steps.stage = smem + L::kOffStage + warp * kStages * kStageBytes;
+    steps.bar = reinterpret_cast<uint64_t *>(smem + L::kOffBar) + warp * kStages;
+    steps.valid = reinterpret_cast<uint32_t *>(smem + L::kOffValid) + warp * kStages;
+    steps.issued = steps.used = 0;
+    steps.dead = false;
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i) mbar_init(steps.bar + i, 1);
+    Walk<R, kThreads> w;
+    w.start(a, reinterpret_cast<int64_t *>(smem + L::kOffScratch));
+    Cut *const cut = reinterpret_cast<Cut *>(a.ws + (int64_t)blockIdx.x * kCutBytes);
+    if (tid == 0) cut->cut = 0;
+    if (blockIdx.x == 0)
+        for (int b = tid; b < a.batch; b += kThreads)
+            if (__ldg(a.kv_len + b) > (a.pages_per_seq << a.pools.shift)) atomicOr(&g_fault, tq3::kFaultPoolIndex);
+
+    for (; !w.done(); w.next(a)) {
+        const Seq s = w.seq;
+        const int rows = s.new_tokens * a.group, r0 = w.block * R, before = s.keys - s.new_tokens;
+        const int p_lo = before + r0 / a.group, p_hi = before + (min(r0 + R, rows) - 1) / a.group;
+        const int take = w.take();
+
+        // the page entries of 32 steps at a time, a lane each
+        int32_t pages = -1;
+        auto sub = [&](int i) { return w.span.tile(w.tile + i) * kTileKeys + warp * kSub; };
+        auto seen = [&](int j0) { return j0 <= p_hi && (j0 + kSub > w.span.from || j0 < w.span.until); };
+        auto load_pages = [&](int i) {
+            pages = -1;
+            if (a.pools.shift >= 4 && i + lane < take) {
+                const int j0 = sub(i + lane);
+                if (seen(j0)) pages = __ldg(a.table + w.b * a.pages_per_seq + (j0 >> a.pools.shift));
+            }
+        };
+        int ahead = 0;  // the next step to request
+        auto request = [&]() {
+            while (ahead < take && steps.issued - steps.used < kStages && !steps.dead) {
+                if ((ahead & 31) == 0) load_pages(ahead);
+                const int j0 = sub(ahead);
+                const int32_t page = __shfl_sync(0xffffffffu, pages, ahead & 31);
+                if (seen(j0)) steps.issue(a, w.b, w.head, j0, p_hi, w.span.from, w.span.until, page, lane);
+                ++ahead;
+            }
+        };
+        request();
+
+        // q~ of the block's rows, scaled by the power of two that brings the largest to 2^13 .. 2^14
+        float down;
+        {
+            float v[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                load_row(a, s, w.head, r0 + 8 * n + warp, lane, v[n]);
+                row_fwht(v[n], lane);
+                float m = fmaxf(fmaxf(fabsf(v[n][0]), fabsf(v[n][1])), fmaxf(fabsf(v[n][2]), fabsf(v[n][3])));
+#pragma unroll
+                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (lane == 0) top[8 * n + warp] = m < INFINITY ? m : 0.0f;  // such a row spoils only itself
+            }
+            __syncthreads();
+            float m = 0.0f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) m = fmaxf(m, top[r]);
+            // 2^(13 - e) and its reciprocal, of biased exponents 267 - e and e - 13 (up to 2^127)
+            const int e = max(14, min(253, (int)(__float_as_uint(m) >> 23)));
+            const int up_exp = min(254, 267 - e);
+            const float up = __uint_as_float((uint32_t)up_exp << 23);
+            down = __uint_as_float((uint32_t)(254 - up_exp) << 23);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = __fmul_rn(v[n][i], up);
+                uint2 hi = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
+                __half *const to = qs + (8 * n + warp) * 136 + 4 * lane;
+                *reinterpret_cast<uint2 *>(to) = hi;
+                if (kWide)
+                    *reinterpret_cast<uint2 *>(to + L::kQ) =
+                        make_uint2(residue_half2(x[0], x[1], hi.x), residue_half2(x[2], x[3], hi.y));
+            }
+            __syncthreads();
+        }
+        const float coef = __fmul_rn(__fmul_rn(a.coef, 1.0f / kGain), down);
+        // lane (g, t): row g, coordinates 32 t .. 32 t + 31, as the B operands of eight products
+        uint32_t qh[NT][8][2], ql[NT][kWide ? 8 : 1][2];
+        int p[NT][2];  // positions of rows 2 t and 2 t + 1
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const __half *const from = qs + (8 * n + g) * 136 + 32 * t;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(from + 4 * j);
+                qh[n][j][0] = x.x, qh[n][j][1] = x.y;
+                if (kWide) {
+                    const uint2 y = *reinterpret_cast<const uint2 *>(from + L::kQ + 4 * j);
+                    ql[n][kWide ? j : 0][0] = y.x, ql[n][kWide ? j : 0][1] = y.y;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = r0 + 8 * n + 2 * t + e;
+                p[n][e] = r < rows ? before + r / a.group : -1;
+            }
+        }
+        float acc[NT][8][4], M[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.0f;
+            M[n][0] = M[n][1] = -FLT_MAX;
+            l[n][0] = l[n][1] = 0.0f;
+        }
+
+        for (int i = 0; i < take && !steps.dead; ++i) {
+            const int j0 = sub(i);
+            if (!seen(j0)) continue;
+            if (!steps.arrived(lane)) {
+                steps.dead = true;
+                break;
+            }
+            const int st = steps.used % kStages;
+            const uint32_t *const rec = reinterpret_cast<const uint32_t *>(steps.stage + st * kStageBytes);
+            const uint32_t valid = steps.valid[st];
+            // keys g and g + 8: words 3 t .. 3 t + 2 of the indices, the key's and the value's factors
+            uint32_t ka[3], kb[3];
+#pragma unroll
+            for (int x = 0; x < 3; ++x) ka[x] = rec[14 * g + 3 * t + x], kb[x] = rec[14 * (g + 8) + 3 * t + x];
+            const float2 fa = *reinterpret_cast<const float2 *>(rec + 14 * g + 12),
+                         fb = *reinterpret_cast<const float2 *>(rec + 14 * (g + 8) + 12);
+            const uint32_t *const vrec = rec + 14 * kSub;
+            const float2 ga = *reinterpret_cast<const float2 *>(vrec + 14 * g + 12),
+                         gb = *reinterpret_cast<const float2 *>(vrec + 14 * (g + 8) + 12);
+            // values of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: coordinates 16 g .. 16 g + 15, bits 48 g on
+            uint32_t v[4][2];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t *const from = vrec + 14 * (2 * t + (x & 1) + 8 * (x >> 1)) + (3 * g >> 1);
+                const uint32_t lo = from[0], hi = from[1];
+                // as two groups of 24 bits
+                v[x][0] = (g & 1) ? __funnelshift_r(lo, hi, 16) : lo;
+                v[x][1] = (g & 1) ? hi >> 8 : __funnelshift_r(lo, hi, 24);
+            }
+            __syncwarp();
+            ++steps.used;
+            request();
+
+            float S[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[n][e] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const Pair<kWide> a0 = lookup<kWide>(table, column, field(ka, 12 * j)),
+                                  a1 = lookup<kWide>(table, column, field(kb, 12 * j)),
+                                  a2 = lookup<kWide>(table, column, field(ka, 12 * j + 6)),
+                                  a3 = lookup<kWide>(table, column, field(kb, 12 * j + 6));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) product<NT, kWide>(S[n], a0, a1, a2, a3, qh[n][j], ql[n][kWide ? j : 0]);
+            }
+            // s + log2 g and 1 / g of keys g, g + 8
+            const float f[2] = {__fmul_rn(__fmul_rn(fa.x, fa.y), coef), __fmul_rn(__fmul_rn(fb.x, fb.y), coef)};
+            float lg[2], inv[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float gv = x ? __fmul_rn(gb.x, gb.y) : __fmul_rn(ga.x, ga.y);
+                gv = gv < kTiny ? kTiny : gv;
+                lg[x] = lg2(gv), inv[x] = rcp(gv);
+            }
+            // 0 where the weight is masked: an infinite or NaN factor must not reach the row's sum
+            float live[NT][4];
+            const bool whole = valid == 0xffffu && j0 + kSub <= p_lo + 1 &&
+                               (a.window == 0 || j0 > p_hi - a.window || j0 + kSub <= a.sinks);
+            bool raise = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int x = e >> 1;
+                    S[n][e] = __fmaf_rn(S[n][e], f[x], lg[x]);
+                    live[n][e] = inv[x];
+                    if (!whole) {
+                        const int key = g + 8 * x, j = j0 + key, pos = p[n][e & 1];
+                        const bool on = ((valid >> key) & 1u) && j <= pos &&
+                                        (a.window == 0 || j > pos - a.window || j < a.sinks);
+                        if (!on) S[n][e] = -INFINITY, live[n][e] = 0.0f;
+                    }
+                    raise |= S[n][e] > __fadd_rn(M[n][e & 1], kLazy);
+                }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float alpha[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = fmaxf(S[n][e], S[n][e + 2]);
+#pragma unroll
+                        for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        m = fmaxf(m, M[n][e]);
+                        alpha[e] = ex2(__fsub_rn(M[n][e], m));
+                        M[n][e] = m;
+                        l[n][e] = __fmul_rn(l[n][e], alpha[e]);
+                    }
+#pragma unroll
+                    for (int i2 = 0; i2 < 8; ++i2)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[n][i2][e] = __fmul_rn(acc[n][i2][e], alpha[e & 1]);
+                }
+            }
+            uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float e4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    e4[e] = ex2(__fsub_rn(S[n][e], __fsub_rn(M[n][e & 1], kLift)));
+                    l[n][e & 1] = __fmaf_rn(e4[e], live[n][e], l[n][e & 1]);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t hi = pack_half2(e4[2 * x], e4[2 * x + 1]);
+                    ph[n][x] = transpose8x8(hi);
+                    pl[n][x] = kWide ? transpose8x8(residue_half2(e4[2 * x], e4[2 * x + 1], hi)) : 0u;
+                }
+            }
+            // per 8 coordinates: pairs (key 2 t, key 2 t + 1) of one coordinate, even ones and odd ones
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t even = 0x1c71c7u, odd = even << 3;
+                const uint32_t e0[1] = {(v[0][h] & even) | ((v[1][h] << 3) & odd)},
+                               o0[1] = {((v[0][h] >> 3) & even) | (v[1][h] & odd)},
+                               e1[1] = {(v[2][h] & even) | ((v[3][h] << 3) & odd)},
+                               o1[1] = {((v[2][h] >> 3) & even) | (v[3][h] & odd)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const Pair<kWide> a0 = lookup<kWide>(table, column, field(e0, 6 * c)),
+                                      a1 = lookup<kWide>(table, column, field(o0, 6 * c)),
+                                      a2 = lookup<kWide>(table, column, field(e1, 6 * c)),
+                                      a3 = lookup<kWide>(table, column, field(o1, 6 * c));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) product<NT, kWide>(acc[n][4 * h + c], a0, a1, a2, a3, ph[n], pl[n]);
+                }
+            }
+        }
+
+        // join the warps: row r by warp r % 8
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float x = l[n][e];
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
+                const int r = 8 * n + 2 * t + e;
+                if (g == 0) *reinterpret_cast<float2 *>(stat + 2 * (warp * R + r)) = make_float2(M[n][e], x);
+                float *const to = merge + (warp * R + r) * 132 + 16 * g;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<float2 *>(to + 2 * i) = make_float2(acc[n][i][e], acc[n][i][e + 2]);
+            }
+        __syncthreads();
+        const bool whole = w.tile == 0 && take == w.segment();
+        float *const slot = slot_at<R>(a, gridDim.x, 2 * blockIdx.x + (w.tile == 0));
+        if (!whole && w.tile == 0 && tid == 0) {
+            Cut c;
+            c.total = w.total, c.end = w.at + w.segment(), c.cut = 1, c.seq = w.b, c.head = w.head, c.block = w.block;
+            *cut = c;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = 8 * n + warp;
+            if (r0 + r >= rows) continue;
+            float m = -FLT_MAX, sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) m = fmaxf(m, stat[2 * (x * R + r)]);
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                const float2 ml = *reinterpret_cast<const float2 *>(stat + 2 * (x * R + r));
+                const float f = ex2(__fsub_rn(ml.x, m));
+                const float4 o = *reinterpret_cast<const float4 *>(merge + (x * R + r) * 132 + 4 * lane);
+                sum = __fmaf_rn(ml.y, f, sum);
+                v[0] = __fmaf_rn(o.x, f, v[0]);
+                v[1] = __fmaf_rn(o.y, f, v[1]);
+                v[2] = __fmaf_rn(o.z, f, v[2]);
+                v[3] = __fmaf_rn(o.w, f, v[3]);
+            }
+            const float f = sum == 0.0f ? 0.0f : __fmul_rn(__frcp_rn(sum), 1.0f / kGain);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], f);
+            if (whole) {
+                store_row(a, s, w.head, r0 + r, lane, v);
+            } else {
+                *reinterpret_cast<float4 *>(slot + r * 128 + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+                if (lane == 0) slot[R * 128 + r] = sum == 0.0f ? -INFINITY : m, slot[R * 129 + r] = sum;
+            }
+        }
+        __syncthreads();
+    }
+    // no copy outlives the CTA
+    while (steps.used != steps.issued) {
+        mbar_wait_bounded(steps.bar + steps.used % kStages, (steps.used / kStages) & 1u, kMaxPolls);
+        ++steps.used;
+    }
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args a) {
+    merge_cut<R, kThreads>(a, gridDim.x);
+}
+
+unsigned int read_and_clear_fault() {
+    unsigned int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_fault, sizeof v) != cudaSuccess) return 0x80000000u;
+    if (v) cudaMemcpyToSymbol(g_fault, &zero, sizeof zero);
+    return v;
+}
+
+constexpr int kParts = 2 * kSms;
+
+template <int NT, bool kWide>
+wq_status run_rows(const Args &a, cudaStream_t s) {
+    using L = Layout<NT, kWide>;
+    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(rows_kernel<NT, kWide>), L::kBytes)) return WQ_ERR_CUDA;
+    rows_kernel<NT, kWide><<<kParts, kThreads, L::kBytes, s>>>(a);
+    join_kernel<L::kRows><<<kParts, kThreads, 0, s>>>(a);
+    return launch_status();
+}
+
+}  // namespace tq3_chunk
+}  // namespace wq
+
+using namespace wq;
+
+extern "C" int64_t tq3_attention_chunk_workspace(int64_t max_q, int64_t group) {
+    if (max_q < 0 || group < 1) return -1;
+    return tq3_chunk::workspace_bytes<8>(tq3_chunk::kParts);
+}
+
+extern "C" wq_status tq3_attention_chunk(const void *q, int q_dtype, int64_t n_tokens, int64_t q_heads,
+                                         int64_t q_token_stride, int64_t q_head_stride, const uint8_t *k_pool,
+                                         const uint8_t *v_pool, int64_t n_pages, int64_t kv_heads, int64_t page_size,
+                                         const int32_t *page_table, int64_t batch, int64_t pages_per_seq,
+                                         const int32_t *q_start, const int32_t *kv_len, int64_t max_q, int64_t window,
+                                         int64_t sinks, const uint32_t *sign_mask, float softmax_scale, void *out,
+                                         int out_dtype, void *workspace, int64_t workspace_bytes, void *stream) {
+    if (n_tokens < 0 || n_tokens > INT32_MAX || batch < 0 || batch > INT32_MAX || pages_per_seq < 0 ||
+        pages_per_seq > (int64_t(1) << 31) || max_q < 0 || window < 0 || window > INT32_MAX || sinks < 0 ||
+        sinks > INT32_MAX || !(fabsf(softmax_scale) < INFINITY))
+        return WQ_ERR_SHAPE;
+    if (!tq3_cache::pool_shape_ok(n_pages, kv_heads, page_size)) return WQ_ERR_SHAPE;
+    if (q_heads < kv_heads || q_heads % kv_heads) return WQ_ERR_SHAPE;
+    const int64_t group = q_heads / kv_heads;
+    if (group > INT32_MAX || n_tokens > (INT32_MAX - 4096) / group) return WQ_ERR_SHAPE;
+    const int64_t most = int64_t(1) << 40;
+    for (int64_t s : {q_token_stride, q_head_stride})
+        if (s < 0 || s > most || (n_tokens && s > (int64_t(1) << 59) / n_tokens)) return WQ_ERR_SHAPE;
+    if (!valid_dtype(q_dtype) || !valid_dtype(out_dtype)) return WQ_ERR_DTYPE;
+    if (n_tokens == 0 || batch == 0) return WQ_OK;
+    if (!q || !k_pool || !v_pool || !page_table || !q_start || !kv_len || !sign_mask || !out || !workspace)
+        return WQ_ERR_NULL;
+    if (workspace_bytes < tq3_attention_chunk_workspace(max_q, group)) return WQ_ERR_SHAPE;
+    const int64_t size = dtype_size(q_dtype);
+    if (q_token_stride * size % 16 || q_head_stride * size % 16) return WQ_ERR_ALIGN;
+    if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(page_table, 4) ||
+        !aligned(q_start, 4) || !aligned(kv_len, 4) || !aligned(out, 16) || !aligned(workspace, 16))
+        return WQ_ERR_ALIGN;
+    tq3_chunk::Args a;
+    a.q = q, a.q_token = q_token_stride, a.q_head = q_head_stride;
+    a.pools = tq3_cache::Pools{const_cast<uint8_t *>(k_pool), const_cast<uint8_t *>(v_pool), n_pages, (int)kv_heads,
+                               tq3_cache::page_shift(page_size)};
+    a.table = page_table, a.q_start = q_start, a.kv_len = kv_len, a.pages_per_seq = pages_per_seq;
+    a.batch = (int)batch, a.n_tokens = (int)n_tokens, a.group = (int)group;
+    a.window = (int)window, a.sinks = (int)sinks;
+    a.rows_from = 0, a.rows_to = INT32_MAX;
+    // post * softmax_scale * log2(e), rounded once
+    a.coef = (float)(0.08838834764831844055 * (double)softmax_scale * 1.4426950408889634074);
+    for (int i = 0; i < 4; ++i) a.mask.w[i] = sign_mask[i];
+    a.out = out, a.q_bf16 = q_dtype == WQ_BF16, a.out_bf16 = out_dtype == WQ_BF16;
+    a.ws = static_cast<unsigned char *>(workspace);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool wide = !a.q_bf16 || !a.out_bf16;
+    return wide ? tq3_chunk::run_rows<1, true>(a, s) : tq3_chunk::run_rows<1, false>(a, s);
+}

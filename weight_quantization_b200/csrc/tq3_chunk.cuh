@@ -1,0 +1,328 @@
+// Attention of ragged chunks of new tokens over a batch's paged TQ3 cache: what its kernels share.
+// Internal to libwq_b200.
+//
+// The rows of (sequence, KV head) are its new tokens' query heads of that KV head, token by token:
+// row r is token r / group, query head h * group + r % group. A segment is a block of R consecutive
+// rows of one (sequence, KV head); its work is the list of 128-key tiles that any of its rows sees.
+// All tiles of all segments, in the order (sequence, KV head, block, tile), are one line of work that
+// is cut into equal parts, one per CTA, whatever the sequences' lengths. Each CTA finds its part from
+// q_start and kv_len alone. A segment inside one part is finished there; one that is cut leaves a
+// partial result per part (rows normalised by their own sums, with the maxima and sums), which
+// merge_kernel joins in the order of the parts: the result does not depend on timing.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "tq3_cache.cuh"
+#include "tq3_common.cuh"
+
+namespace wq {
+namespace tq3_chunk {
+
+using tq3::SignMask;
+
+constexpr int kTileKeys = 128;
+constexpr int kSms = 148;
+constexpr int kMaxKeys = 0x7fffffff - 4096;  // keys of a sequence: tile arithmetic stays within int32
+
+struct Args {
+    const void *q;
+    int64_t q_token, q_head;  // strides in elements
+    tq3_cache::Pools pools;
+    const int32_t *table, *q_start, *kv_len;
+    int64_t pages_per_seq;
+    int batch, n_tokens, group;
+    int window, sinks;  // window == 0: none
+    int rows_from, rows_to;  // serves the sequences with rows_from <= rows per KV head < rows_to
+    float coef;              // post * softmax_scale * log2(e)
+    SignMask mask;
+    void *out;
+    int q_bf16, out_bf16;
+    unsigned char *ws;
+};
+
+// A sequence's new tokens and keys, as this launch serves it.
+struct Seq {
+    int start, new_tokens, keys;
+};
+
+__device__ __forceinline__ int clamp_int(int64_t v, int64_t lo, int64_t hi) {
+    return (int)(v < lo ? lo : v > hi ? hi : v);
+}
+
+__device__ __forceinline__ Seq load_seq(const Args &a, int b) {
+    Seq s;
+    s.start = clamp_int(__ldg(a.q_start + b), 0, a.n_tokens);
+    s.new_tokens = clamp_int(__ldg(a.q_start + b + 1), s.start, a.n_tokens) - s.start;
+    const int64_t room = a.pages_per_seq << a.pools.shift;
+    s.keys = clamp_int(__ldg(a.kv_len + b), 0, room < kMaxKeys ? room : kMaxKeys);
+    const int64_t rows = (int64_t)s.new_tokens * a.group;
+    if (rows < a.rows_from || rows >= a.rows_to) s.new_tokens = 0;
+    return s;
+}
+
+// The tiles that rows at positions p_lo .. p_hi see: `sinks` tiles from key 0 on, then the tiles from
+// `first` on, `n` in all. Keys below `from` are seen only as sinks (below `until`).
+struct Span {
+    int sinks, first, n;
+    int from, until;
+    __device__ __forceinline__ int tile(int i) const { return i < sinks ? i : first + i - sinks; }
+};
+
+__device__ __forceinline__ Span span_of(const Args &a, int p_lo, int p_hi) {
+    Span s;
+    s.from = a.window && p_lo >= a.window ? p_lo - a.window + 1 : 0;
+    s.until = min(a.sinks, s.from);
+    s.first = s.from / kTileKeys;
+    s.sinks = min((s.until + kTileKeys - 1) / kTileKeys, s.first);
+    s.n = p_hi < 0 ? 0 : s.sinks + p_hi / kTileKeys - s.first + 1;
+    return s;
+}
+
+template <int R>
+__device__ __forceinline__ Span block_span(const Args &a, const Seq &s, int block) {
+    const int r0 = block * R, r1 = min(r0 + R, s.new_tokens * a.group) - 1;
+    const int before = s.keys - s.new_tokens;
+    return span_of(a, before + r0 / a.group, before + r1 / a.group);
+}
+
+// A block without a visible key still counts one tile: its rows are written as zeros.
+template <int R>
+__device__ __forceinline__ int blocks_of(const Args &a, const Seq &s) {
+    return (s.new_tokens * a.group + R - 1) / R;
+}
+template <int R>
+__device__ __forceinline__ int64_t tiles_of_head(const Args &a, const Seq &s) {
+    int64_t n = 0;
+    for (int i = blocks_of<R>(a, s) - 1; i >= 0; --i) n += max(1, block_span<R>(a, s, i).n);
+    return n;
+}
+
+// Header of a part whose last segment is cut, written by that part's CTA for merge_kernel.
+struct Cut {
+    int64_t total;     // tiles of the whole launch
+    int64_t end;       // where on the line the segment ends
+    int cut, seq, head, block;
+};
+constexpr int kCutBytes = 64;
+
+template <int R>
+__host__ __device__ constexpr int64_t slot_floats() {
+    return R * (128 + 2);
+}
+// Slot 2c: the segment that part c continues; 2c + 1: the one that it begins and does not finish.
+template <int R>
+__device__ __forceinline__ float *slot_at(const Args &a, int parts, int i) {
+    return reinterpret_cast<float *>(a.ws + (int64_t)parts * kCutBytes) + i * slot_floats<R>();
+}
+template <int R>
+constexpr int64_t workspace_bytes(int64_t parts) {
+    return parts * (kCutBytes + 2 * slot_floats<R>() * 4);
+}
+
+__device__ __forceinline__ int64_t part_begin(int64_t total, int part, int parts) { return total * part / parts; }
+
+// Walks this CTA's part of the line. All threads of the CTA hold the same state.
+template <int R, int kThreads>
+struct Walk {
+    int64_t total, at, end;  // on the line
+    int b, head, block, blocks, tile;  // tile: the first one of the segment that is this CTA's
+    Seq seq;
+    Span span;
+
+    // `scratch`: kThreads / 32 + 2 int64 in shared memory.
+    __device__ __forceinline__ void start(const Args &a, int64_t *scratch) {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        constexpr int kWarps = kThreads / 32;
+        int64_t mine = 0, first = 0;
+        for (int i = tid; i < a.batch; i += kThreads) {
+            const int64_t c = tiles_of_head<R>(a, load_seq(a, i)) * a.pools.heads;
+            if (i == tid) first = c;
+            mine += c;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (lane == 0) scratch[warp] = mine;
+        __syncthreads();
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) total += scratch[w];
+        at = part_begin(total, blockIdx.x, gridDim.x);
+        end = part_begin(total, blockIdx.x + 1, gridDim.x);
+        __syncthreads();
+        if (at >= end) return;
+        // the sequence that holds `at`, by a prefix sum over kThreads sequences at a time
+        int64_t before = 0;
+        for (int base = 0;; base += kThreads) {
+            const int i = base + tid;
+            const int64_t c = base == 0 ? first : i < a.batch ? tiles_of_head<R>(a, load_seq(a, i)) * a.pools.heads : 0;
+            int64_t sum = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (lane == 31) scratch[warp] = sum;
+            __syncthreads();
+            int64_t lead = before;
+            for (int w = 0; w < warp; ++w) lead += scratch[w];
+            int64_t all = before;
+            for (int w = 0; w < kWarps; ++w) all += scratch[w];
+            if (at >= lead + sum - c && at < lead + sum) {
+                scratch[kWarps] = i;
+                scratch[kWarps + 1] = at - (lead + sum - c);
+            }
+            __syncthreads();
+            before = all;
+            if (at < all) break;
+        }
+        b = (int)scratch[kWarps];
+        int64_t off = scratch[kWarps + 1];
+        seq = load_seq(a, b);
+        blocks = blocks_of<R>(a, seq);
+        const int64_t per_head = tiles_of_head<R>(a, seq);
+        head = (int)(off / per_head);
+        off -= head * per_head;
+        block = 0;
+        for (;; ++block) {
+            span = block_span<R>(a, seq, block);
+            const int n = max(1, span.n);
+            if (off < n) break;
+            off -= n;
+        }
+        tile = (int)off;
+        __syncthreads();
+    }
+    __device__ __forceinline__ bool done() const { return at >= end; }
+    __device__ __forceinline__ int segment() const { return max(1, span.n); }
+    __device__ __forceinline__ int take() const {
+        const int64_t n = segment() - tile, left = end - at;
+        return (int)(n < left ? n : left);
+    }
+    __device__ __forceinline__ void next(const Args &a) {
+        at += take();
+        if (at >= end) return;
+        tile = 0;
+        if (++block == blocks) {
+            block = 0;
+            if (++head == a.pools.heads) {
+                head = 0;
+                do {
+                    seq = load_seq(a, ++b);
+                } while (seq.new_tokens == 0);
+                blocks = blocks_of<R>(a, seq);
+            }
+        }
+        span = block_span<R>(a, seq, block);
+    }
+};
+
+// 128-point Walsh-Hadamard transform (unnormalised) of a row that a warp holds, lane l elements
+// 4 l .. 4 l + 3.
+__device__ __forceinline__ void row_fwht(float (&v)[4], int lane) {
+    {
+        const float a = __fadd_rn(v[0], v[1]), b = __fsub_rn(v[0], v[1]), c = __fadd_rn(v[2], v[3]),
+                    d = __fsub_rn(v[2], v[3]);
+        v[0] = __fadd_rn(a, c);
+        v[1] = __fadd_rn(b, d);
+        v[2] = __fsub_rn(a, c);
+        v[3] = __fsub_rn(b, d);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float w = __shfl_xor_sync(0xffffffffu, v[i], o);
+            v[i] = (lane & o) ? __fsub_rn(w, v[i]) : __fadd_rn(v[i], w);
+        }
+}
+
+__device__ __forceinline__ float sign_of(const SignMask &m, int e) {
+    return __uint_as_float(0x3f800000u | (~(m.w[e >> 5] >> (e & 31)) & 1u) << 31);
+}
+
+// Elements 4 l .. 4 l + 3 of row `row` of (sequence, head), with the sign flips; zeros past the rows.
+__device__ __forceinline__ void load_row(const Args &a, const Seq &s, int head, int row, int lane, float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = 0.0f;
+    if (row < s.new_tokens * a.group) {
+        const int64_t at = (int64_t)(s.start + row / a.group) * a.q_token +
+                           (int64_t)(head * a.group + row % a.group) * a.q_head + 4 * lane;
+        if (a.q_bf16) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + at));
+            v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+        } else {
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at));
+            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], sign_of(a.mask, 4 * lane + i));
+}
+
+// out = s . H(row) post, from the rotated basis.
+__device__ __forceinline__ void store_row(const Args &a, const Seq &s, int head, int row, int lane, float (&v)[4]) {
+    row_fwht(v, lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], tq3::fwht_post()), sign_of(a.mask, 4 * lane + i));
+    const int64_t at = ((int64_t)(s.start + row / a.group) * a.pools.heads * a.group + head * a.group + row % a.group) * 128 +
+                       4 * lane;
+    if (a.out_bf16)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Joins the partial results of the segments that parts leave cut (one CTA per part; kThreads / 32
+// warps, a row each).
+template <int R, int kThreads>
+__device__ __forceinline__ void merge_cut(const Args &a, int parts) {
+    const int part = blockIdx.x, lane = threadIdx.x & 31;
+    const Cut c = *reinterpret_cast<const Cut *>(a.ws + (int64_t)part * kCutBytes);
+    if (!c.cut) return;
+    const Seq s = load_seq(a, c.seq);
+    const int rows = min(R, s.new_tokens * a.group - c.block * R);
+    // parts after this one up to the segment's end; an empty part has no slot
+    int last = part + 1;
+    while (last < parts && part_begin(c.total, last, parts) < c.end) ++last;
+    for (int r = threadIdx.x >> 5; r < rows; r += kThreads / 32) {
+        float top = -INFINITY;
+        for (int p = part + lane; p < last; p += 32) {
+            if (p > part && part_begin(c.total, p, parts) == part_begin(c.total, p + 1, parts)) continue;
+            top = fmaxf(top, slot_at<R>(a, parts, 2 * p + (p == part))[R * 128 + r]);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
+        if (top != -INFINITY)
+            for (int p = part; p < last; ++p) {
+                if (p > part && part_begin(c.total, p, parts) == part_begin(c.total, p + 1, parts)) continue;
+                const float *const slot = slot_at<R>(a, parts, 2 * p + (p == part));
+                const float w = __fmul_rn(slot[R * 129 + r], ex2(__fsub_rn(slot[R * 128 + r], top)));
+                const float4 x = *reinterpret_cast<const float4 *>(slot + r * 128 + 4 * lane);
+                sum = __fadd_rn(sum, w);
+                v[0] = __fmaf_rn(w, x.x, v[0]);
+                v[1] = __fmaf_rn(w, x.y, v[1]);
+                v[2] = __fmaf_rn(w, x.z, v[2]);
+                v[3] = __fmaf_rn(w, x.w, v[3]);
+            }
+        if (sum != 0.0f) {
+            const float f = __frcp_rn(sum);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], f);
+        }
+        store_row(a, s, c.head, c.block * R + r, lane, v);
+    }
+}
+
+}  // namespace tq3_chunk
+}  // namespace wq

@@ -35,6 +35,9 @@ PROTOTYPES = {
     "tq3_cache_append": (_int, [_vp, _vp, _int, _i64, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64,
                                 _vp]),
     "tq3_cache_read": (_int, [_vp, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _int, _vp]),
+    "tq3_attention_chunk": (_int, [_vp, _int, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp,
+                                   _vp, _i64, _i64, _i64, _vp, C.c_float, _vp, _int, _vp, _i64, _vp]),
+    "tq3_attention_chunk_workspace": (_i64, [_i64, _i64]),
     "tq3_compressed_bytes": (_i64, [_i64]),
     "rpbh_quantize_weight": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _int, _vp, _vp, _vp, _vp]),
     "rpbh_requantize_weight": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _int, _vp, _vp, _vp, _int, _vp]),
@@ -415,6 +418,47 @@ def tq3_cache_read(k_pool: torch.Tensor, v_pool: torch.Tensor, page_table: torch
                                   _DT[k_out.dtype], _stream(device))
     _check("tq3_cache_read", st)
     return k_out, v_out
+
+
+def tq3_attention_chunk(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, page_table: torch.Tensor,
+                        q_start: torch.Tensor, kv_len: torch.Tensor, sign_mask, max_q=None, window: int = 0,
+                        sinks: int = 0, softmax_scale: float = 128 ** -0.5, out_dtype=None, out=None):
+    """Causal attention of ragged chunks of new tokens over a batch's paged cache (as tq3_cache_append
+    writes it, the new tokens included): rows q_start[b] .. q_start[b + 1] - 1 (int32 [batch + 1],
+    ascending) of q [tokens, q_heads, 128] (fp32/bf16; a slice of a fused projection will do) are the
+    last tokens of sequence b, whose kv_len[b] (int32 [batch]) keys are reached through page_table int32
+    [batch, pages_per_seq]. With window > 0 a token at position p sees only the keys j > p - window and
+    the first `sinks` ones; entries of pages that no row sees are not read. max_q: how many new tokens a
+    sequence has at most (default: all of q). Tokens that see no key get zeros, rows of no sequence are left as
+    they were, keys without a page in the pool are masked out and raise device fault bit 6. Returns out
+    [tokens, q_heads, 128]."""
+    qp, q_token, q_head = _rows128(q, "q")
+    n_pages, heads, page_size = _cache_pools(k_pool, v_pool, q.device)
+    tokens, q_heads = q.shape[:2]
+    if heads < 1 or q_heads < heads or q_heads % heads:
+        raise ValueError("q's heads must be a multiple of the pools' heads")
+    batch, pages_per_seq = _cache_table(page_table, q.device)
+    for name, t, n in (("q_start", q_start, batch + 1), ("kv_len", kv_len, batch)):
+        _on(t, q.device, name, (torch.int32,))
+        if t.numel() != n:
+            raise ValueError(f"{name} must be int32 [{n}]")
+    if out is None:
+        out = torch.empty((tokens, q_heads, 128), dtype=out_dtype or q.dtype, device=q.device)
+    _on(out, q.device, "out", _DT)
+    _fits(out, tokens * q_heads * 128, "out")
+    most = tokens if max_q is None else int(max_q)
+    m = _mask_arg(sign_mask)
+    with torch.cuda.device(q.device):
+        need = max(int(lib().tq3_attention_chunk_workspace(most, q_heads // heads)), 0)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        st = lib().tq3_attention_chunk(qp, _DT[q.dtype], tokens, q_heads, q_token, q_head, _dev(k_pool, "k_pool"),
+                                       _dev(v_pool, "v_pool"), n_pages, heads, page_size,
+                                       _dev(page_table, "page_table"), batch, pages_per_seq, _dev(q_start, "q_start"),
+                                       _dev(kv_len, "kv_len"), most, int(window), int(sinks), m.ctypes.data,
+                                       float(softmax_scale), _dev(out, "out"), _DT[out.dtype], ws.data_ptr(), need,
+                                       _stream(q.device))
+    _check("tq3_attention_chunk", st)
+    return out
 
 
 def tq3_compressed_bytes(n_vec: int) -> int:
