@@ -9,7 +9,7 @@
 // so both products are over centroids alone: 8 values, looked up as pairs (6 bits) in a table that
 // every lane has a column of in shared memory (a bank of its own, so no conflict).
 //
-// The rows kernel: a warp takes 16 keys at a time and one to NT times 8 rows of one KV head.
+// The rows kernel: a warp takes 32 keys at a time and one to NT times 8 rows of one KV head.
 // S^T = C_K q~^T and O^T += C_V^T w with m16n8k16: the looked-up pairs are the A operands as they are
 // (the 128 coordinates may be summed in any order, so a lane takes the coordinates whose bits it can
 // read as whole words), and no decoded key or value ever leaves the registers. In log2 units the
@@ -37,11 +37,13 @@
 namespace wq {
 namespace tq3_chunk {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kSub = kTileKeys / kWarps;  // keys of a warp's step
-static_assert(kSub == 16, "one m16n8k16 row block per step");
-constexpr int kStages = 4;
-constexpr int kStageBytes = 2 * kSub * tq3_cache::kRec;  // a step's key records, then its value records
+constexpr int kPiece = 16;                // keys of an m16n8k16's rows; a copy within a page
+static_assert(kSub == 2 * kPiece, "two pieces a step, a lane per key");
+constexpr int kStages = 3;
+constexpr int kPieceBytes = kPiece * tq3_cache::kRec;
+constexpr int kStageBytes = 4 * kPieceBytes;  // a step's key records, then its value records
 constexpr uint32_t kMaxPolls = 1u << 24;
 constexpr float kLazy = 8.0f;   // M_i is raised past this margin (log2 units)
 constexpr float kLift = 6.0f;   // weights are at most 2^(kLazy + kLift) < 65504, so 2^-20 of the largest is still normal
@@ -55,16 +57,19 @@ struct Layout {
     static constexpr int kRows = 8 * NT;
     static constexpr int kTable = kWide ? 64 * 32 * 8 : 64 * 32 * 4;
     static constexpr int kQ = kRows * 136;  // halves, rows padded by 16 bytes
+    // a warp's stages; between segments, its rows' sums (132 floats a row)
+    static constexpr int kWarpBytes = kStages * kStageBytes;
     static constexpr int kOffStage = kTable;
-    static constexpr int kOffQ = kOffStage + kWarps * kStages * kStageBytes;
-    static constexpr int kOffMerge = kOffQ + (kWide ? 2 : 1) * kQ * 2;
-    static constexpr int kOffStat = kOffMerge + kWarps * kRows * 132 * 4;  // per warp and row: M, l
-    static constexpr int kOffTop = kOffStat + kWarps * kRows * 8;          // per row: max |q~|
+    static constexpr int kOffFactor = kOffStage + kWarps * kWarpBytes;  // per warp and key of a step
+    static constexpr int kOffQ = kOffFactor + kWarps * kSub * 16;
+    static constexpr int kOffStat = kOffQ + (kWide ? 2 : 1) * kQ * 2;  // per warp and row: M, l
+    static constexpr int kOffTop = kOffStat + kWarps * kRows * 8;      // per row: max |q~|
     static constexpr int kOffBar = kOffTop + kRows * 4;
-    static constexpr int kOffValid = kOffBar + kWarps * kStages * 8;
-    static constexpr int kOffScratch = kOffValid + kWarps * kStages * 4;
+    static constexpr int kOffValid = kOffBar + kWarps * kStages * 8;  // per warp, stage and piece
+    static constexpr int kOffScratch = kOffValid + kWarps * kStages * 16;
     static constexpr int kBytes = kOffScratch + (kWarps + 2) * 8;
-    static_assert(kOffMerge % 16 == 0 && kOffBar % 8 == 0 && kOffScratch % 8 == 0 && kBytes <= 227 * 1024, "layout");
+    static_assert(kRows * 132 * 4 <= kWarpBytes, "a warp's sums fit its stages");
+    static_assert(kOffQ % 16 == 0 && kOffBar % 8 == 0 && kOffScratch % 8 == 0 && kBytes <= 227 * 1024, "layout");
 };
 
 __device__ __forceinline__ float lg2(float x) {
@@ -147,70 +152,112 @@ __device__ __forceinline__ bool wait_copy(uint64_t *bar, uint32_t phase) {
     return ok || mbar_wait_bounded(bar, phase, kMaxPolls);
 }
 
-// A warp's stream of 16-key steps through its stages.
+// A warp's stream of 32-key steps through its stages. Pieces are requested 32 at a time (16 steps), a
+// lane each: its lane works out where the piece lies and later starts its copies.
 struct Steps {
     unsigned char *stage;  // kStages of kStageBytes
-    uint64_t *bar;
-    uint32_t *valid;  // per stage: bit k = key k has a page
+    uint64_t *bar;         // per stage, two arrivals: a piece each
+    uint2 *info;           // per stage and piece: which of its keys have a page; the step's first key
     uint32_t issued, used;
     bool dead;
+    // of the segment
+    int b, head, take, last, from, until;
+    // of the 32 pieces in hand: steps that are still to be requested (bit 2 i), and this lane's piece
+    int base;
+    uint32_t todo;
+    int j;
+    int32_t page;  // its page, -1 where no row sees the piece, -2 where the page is outside the pool
 
-    // Requests the records of keys j0 .. j0 + 15 that some row sees (j <= last, and from <= j or
-    // j < until). page: the entry that holds all 16, where a page has 16 places or more.
-    __device__ __forceinline__ void issue(const Args &a, int b, int head, int j0, int last, int from, int until,
-                                          int32_t page, int lane) {
-        const int st = issued % kStages;
-        unsigned char *const dst = stage + st * kStageBytes;
-        const tq3_cache::Pools &pools = a.pools;
-        const int shift = pools.shift;
-        if (shift >= 4) {
-            const bool ok = page >= 0 && page < pools.n_pages;
-            if (lane == 0) {
-                valid[st] = ok ? 0xffffu : 0u;
-                if (ok) {
-                    const int64_t at = tq3_cache::record_at(pools, page, head, j0 & ((1 << shift) - 1));
-                    mbar_expect_tx(bar + st, kStageBytes);
-                    bulk_load(dst, pools.k + at, kStageBytes / 2, bar + st);
-                    bulk_load(dst + kStageBytes / 2, pools.v + at, kStageBytes / 2, bar + st);
-                } else {
+    __device__ __forceinline__ bool seen(int j0, int n) const { return j0 <= last && (j0 + n > from || j0 < until); }
+
+    template <class W>
+    __device__ __forceinline__ void begin(const W &w, int p_hi) {
+        b = w.b, head = w.head, take = w.take(), last = p_hi, from = w.span.from, until = w.span.until;
+        base = 0, todo = 0;
+    }
+    template <class W>
+    __device__ __forceinline__ void gather(const Args &a, const W &w, int warp, int lane) {
+        const int i = base + (lane >> 1);
+        bool need = false;
+        page = -1;
+        j = 0;
+        if (i < take) {
+            j = w.span.tile(w.tile + i) * kTileKeys + warp * kSub + (lane & 1) * kPiece;
+            need = seen(j, kPiece);
+            if (need && a.pools.shift >= 4) {
+                page = __ldg(a.table + b * a.pages_per_seq + (j >> a.pools.shift));
+                if (page < 0 || page >= a.pools.n_pages) {
                     atomicOr(&g_fault, tq3::kFaultPoolIndex);
-                    mbar_arrive(bar + st);
-                }
-            }
-        } else {
-            // several pages, a lane each; a record alone is not a multiple of 16 bytes, so pages of one
-            // place are copied by the lanes themselves
-            const int size = 1 << shift, n = kSub >> shift;
-            const int k = lane & (n - 1), jp = j0 + (k << shift);
-            const bool mine = shift == 0 || lane < n;
-            const bool need = mine && jp <= last && (jp + size > from || jp < until);
-            const int32_t p = need ? __ldg(a.table + b * a.pages_per_seq + (jp >> shift)) : -1;
-            const bool ok = need && p >= 0 && p < pools.n_pages;
-            if (need && !ok) atomicOr(&g_fault, tq3::kFaultPoolIndex);
-            const uint32_t keys = __reduce_or_sync(0xffffffffu, ok ? ((1u << size) - 1u) << (k << shift) : 0u);
-            const int64_t at = ok ? tq3_cache::record_at(pools, p, head, 0) : 0;
-            if (lane == 0) valid[st] = keys;
-            if (shift == 0) {
-                uint2 r[7];
-                const uint8_t *const src = (lane < 16 ? pools.k : pools.v) + at;
-                uint2 *const to = reinterpret_cast<uint2 *>(dst + lane * tq3_cache::kRec);
-#pragma unroll
-                for (int i = 0; i < 7; ++i) r[i] = ok ? __ldg(reinterpret_cast<const uint2 *>(src) + i) : make_uint2(0u, 0u);
-#pragma unroll
-                for (int i = 0; i < 7; ++i) to[i] = r[i];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar + st);
-            } else {
-                const uint32_t bytes = tq3_cache::kRec << shift;
-                if (lane == 0) mbar_expect_tx(bar + st, __popc(keys) * 2 * tq3_cache::kRec);
-                __syncwarp();
-                if (ok) {
-                    bulk_load(dst + k * bytes, pools.k + at, bytes, bar + st);
-                    bulk_load(dst + kStageBytes / 2 + k * bytes, pools.v + at, bytes, bar + st);
+                    page = -2;
                 }
             }
         }
-        ++issued;
+        const uint32_t m = __ballot_sync(0xffffffffu, need);
+        todo = (m | m >> 1) & 0x55555555u;
+        base += 16;
+    }
+    template <class W>
+    __device__ __forceinline__ void request(const Args &a, const W &w, int warp, int lane) {
+        while (issued - used < kStages) {
+            if (todo == 0) {
+                if (base >= take || dead) return;
+                gather(a, w, warp, lane);
+                continue;
+            }
+            const int at = __ffs(todo) - 1, st = issued % kStages;
+            todo &= todo - 1;
+            if (a.pools.shift >= 4) {
+                if ((lane & ~1) == at) copy_piece(a, st, lane & 1);
+            } else {
+                copy_small(a, st, __shfl_sync(0xffffffffu, j, at), lane);
+            }
+            ++issued;
+        }
+    }
+    // 16 keys of one page, by the lane that holds it.
+    __device__ __forceinline__ void copy_piece(const Args &a, int st, int half) const {
+        info[2 * st + half] = make_uint2(page >= 0 ? 0xffffu : 0u, (uint32_t)(j - half * kPiece));
+        if (page >= 0) {
+            unsigned char *const dst = stage + st * kStageBytes + half * kPieceBytes;
+            const int64_t at = tq3_cache::record_at(a.pools, page, head, j & ((1 << a.pools.shift) - 1));
+            mbar_expect_tx(bar + st, 2 * kPieceBytes);
+            bulk_load(dst, a.pools.k + at, kPieceBytes, bar + st);
+            bulk_load(dst + 2 * kPieceBytes, a.pools.v + at, kPieceBytes, bar + st);
+        } else {
+            mbar_arrive(bar + st);
+        }
+    }
+    // 32 keys in pages of 1 to 8 places, a page a lane. A record alone is not a multiple of 16 bytes, so
+    // pages of one place are copied by the lanes themselves.
+    __device__ __forceinline__ void copy_small(const Args &a, int st, int j0, int lane) const {
+        const tq3_cache::Pools &pools = a.pools;
+        const int shift = pools.shift, size = 1 << shift, jp = j0 + (lane << shift);
+        const bool need = lane < (kSub >> shift) && seen(jp, size);
+        const int32_t p = need ? __ldg(a.table + b * a.pages_per_seq + (jp >> shift)) : -1;
+        const bool ok = need && p >= 0 && p < pools.n_pages;
+        if (need && !ok) atomicOr(&g_fault, tq3::kFaultPoolIndex);
+        const uint32_t keys = __reduce_or_sync(0xffffffffu, ok ? ((1u << size) - 1u) << (lane << shift) : 0u);
+        const int64_t at = ok ? tq3_cache::record_at(pools, p, head, 0) : 0;
+        unsigned char *const dst = stage + st * kStageBytes + (lane << shift) * tq3_cache::kRec;
+        if (lane < 2) info[2 * st + lane] = make_uint2(keys >> (16 * lane) & 0xffffu, (uint32_t)j0);
+        if (shift == 0) {
+            if (ok)
+#pragma unroll
+                for (int i = 0; i < 7; ++i) {
+                    reinterpret_cast<uint2 *>(dst)[i] = __ldg(reinterpret_cast<const uint2 *>(pools.k + at) + i);
+                    reinterpret_cast<uint2 *>(dst + 2 * kPieceBytes)[i] = __ldg(reinterpret_cast<const uint2 *>(pools.v + at) + i);
+                }
+            __syncwarp();
+            if (lane < 2) mbar_arrive(bar + st);
+        } else {
+            const uint32_t bytes = tq3_cache::kRec << shift;
+            if (lane < 2) mbar_expect_tx(bar + st, __popc(keys >> (16 * lane) & 0xffffu) * 2 * tq3_cache::kRec);
+            __syncwarp();
+            if (ok) {
+                bulk_load(dst, pools.k + at, bytes, bar + st);
+                bulk_load(dst + 2 * kPieceBytes, pools.v + at, bytes, bar + st);
+            }
+        }
     }
     __device__ __forceinline__ bool arrived(int lane) {
         const bool ok = __all_sync(0xffffffffu, wait_copy(bar + used % kStages, (used / kStages) & 1u));
@@ -220,7 +267,7 @@ struct Steps {
 };
 
 template <int NT, bool kWide>
-__global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kernel(const __grid_constant__ Args a) {
     using L = Layout<NT, kWide>;
     constexpr int R = L::kRows;
     // centroids times kGain: for one fp16 the gain at which all four magnitudes are nearest to fp16 numbers
@@ -231,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
     unsigned char *const table = smem;
     const uint32_t column = lane * (kWide ? 8 : 4);
     __half *const qs = reinterpret_cast<__half *>(smem + L::kOffQ);
-    float *const merge = reinterpret_cast<float *>(smem + L::kOffMerge);
+    float4 *const factor = reinterpret_cast<float4 *>(smem + L::kOffFactor) + warp * kSub;
     float *const stat = reinterpret_cast<float *>(smem + L::kOffStat);
     float *const top = reinterpret_cast<float *>(smem + L::kOffTop);
 
@@ -245,13 +292,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
             reinterpret_cast<uint32_t *>(table)[i] = hi;
     }
     Steps steps;
-    steps.stage = smem + L::kOffStage + warp * kStages * kStageBytes;
+    steps.stage = smem + L::kOffStage + warp * L::kWarpBytes;
     steps.bar = reinterpret_cast<uint64_t *>(smem + L::kOffBar) + warp * kStages;
-    steps.valid = reinterpret_cast<uint32_t *>(smem + L::kOffValid) + warp * kStages;
+    steps.info = reinterpret_cast<uint2 *>(smem + L::kOffValid) + warp * kStages * 2;
     steps.issued = steps.used = 0;
     steps.dead = false;
     if (lane == 0)
-        for (int i = 0; i < kStages; ++i) mbar_init(steps.bar + i, 1);
+        for (int i = 0; i < kStages; ++i) mbar_init(steps.bar + i, 2);
     Walk<R, kThreads> w;
     w.start(a, reinterpret_cast<int64_t *>(smem + L::kOffScratch));
     Cut *const cut = reinterpret_cast<Cut *>(a.ws + (int64_t)blockIdx.x * kCutBytes);
@@ -266,41 +313,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
         const int p_lo = before + r0 / a.group, p_hi = before + (min(r0 + R, rows) - 1) / a.group;
         const int take = w.take();
 
-        // the page entries of 32 steps at a time, a lane each
-        int32_t pages = -1;
-        auto sub = [&](int i) { return w.span.tile(w.tile + i) * kTileKeys + warp * kSub; };
-        auto seen = [&](int j0) { return j0 <= p_hi && (j0 + kSub > w.span.from || j0 < w.span.until); };
-        auto load_pages = [&](int i) {
-            pages = -1;
-            if (a.pools.shift >= 4 && i + lane < take) {
-                const int j0 = sub(i + lane);
-                if (seen(j0)) pages = __ldg(a.table + w.b * a.pages_per_seq + (j0 >> a.pools.shift));
-            }
-        };
-        int ahead = 0;  // the next step to request
-        auto request = [&]() {
-            while (ahead < take && steps.issued - steps.used < kStages && !steps.dead) {
-                if ((ahead & 31) == 0) load_pages(ahead);
-                const int j0 = sub(ahead);
-                const int32_t page = __shfl_sync(0xffffffffu, pages, ahead & 31);
-                if (seen(j0)) steps.issue(a, w.b, w.head, j0, p_hi, w.span.from, w.span.until, page, lane);
-                ++ahead;
-            }
-        };
-        request();
+        steps.begin(w, p_hi);
+        steps.request(a, w, warp, lane);
 
         // q~ of the block's rows, scaled by the power of two that brings the largest to 2^13 .. 2^14
         float down;
         {
-            float v[NT][4];
+            constexpr int kEach = R / kWarps;
+            float v[kEach][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                load_row(a, s, w.head, r0 + 8 * n + warp, lane, v[n]);
+            for (int n = 0; n < kEach; ++n) {
+                const int r = kWarps * n + warp;
+                load_row(a, s, w.head, r0 + r, lane, v[n]);
                 row_fwht(v[n], lane);
                 float m = fmaxf(fmaxf(fabsf(v[n][0]), fabsf(v[n][1])), fmaxf(fabsf(v[n][2]), fabsf(v[n][3])));
 #pragma unroll
                 for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if (lane == 0) top[8 * n + warp] = m < INFINITY ? m : 0.0f;  // such a row spoils only itself
+                if (lane == 0) top[r] = m < INFINITY ? m : 0.0f;  // such a row spoils only itself
             }
             __syncthreads();
             float m = 0.0f;
@@ -312,12 +341,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
             const float up = __uint_as_float((uint32_t)up_exp << 23);
             down = __uint_as_float((uint32_t)(254 - up_exp) << 23);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < kEach; ++n) {
                 float x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[i] = __fmul_rn(v[n][i], up);
                 uint2 hi = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
-                __half *const to = qs + (8 * n + warp) * 136 + 4 * lane;
+                __half *const to = qs + (kWarps * n + warp) * 136 + 4 * lane;
                 *reinterpret_cast<uint2 *>(to) = hi;
                 if (kWide)
                     *reinterpret_cast<uint2 *>(to + L::kQ) =
@@ -358,81 +387,78 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
             l[n][0] = l[n][1] = 0.0f;
         }
 
-        for (int i = 0; i < take && !steps.dead; ++i) {
-            const int j0 = sub(i);
-            if (!seen(j0)) continue;
-            if (!steps.arrived(lane)) {
+        while (steps.used != steps.issued) {
+            if (steps.dead || !steps.arrived(lane)) {
                 steps.dead = true;
                 break;
             }
             const int st = steps.used % kStages;
             const uint32_t *const rec = reinterpret_cast<const uint32_t *>(steps.stage + st * kStageBytes);
-            const uint32_t valid = steps.valid[st];
-            // keys g and g + 8: words 3 t .. 3 t + 2 of the indices, the key's and the value's factors
-            uint32_t ka[3], kb[3];
-#pragma unroll
-            for (int x = 0; x < 3; ++x) ka[x] = rec[14 * g + 3 * t + x], kb[x] = rec[14 * (g + 8) + 3 * t + x];
-            const float2 fa = *reinterpret_cast<const float2 *>(rec + 14 * g + 12),
-                         fb = *reinterpret_cast<const float2 *>(rec + 14 * (g + 8) + 12);
             const uint32_t *const vrec = rec + 14 * kSub;
-            const float2 ga = *reinterpret_cast<const float2 *>(vrec + 14 * g + 12),
-                         gb = *reinterpret_cast<const float2 *>(vrec + 14 * (g + 8) + 12);
-            // values of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: coordinates 16 g .. 16 g + 15, bits 48 g on
-            uint32_t v[4][2];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const uint32_t *const from = vrec + 14 * (2 * t + (x & 1) + 8 * (x >> 1)) + (3 * g >> 1);
-                const uint32_t lo = from[0], hi = from[1];
-                // as two groups of 24 bits
-                v[x][0] = (g & 1) ? __funnelshift_r(lo, hi, 16) : lo;
-                v[x][1] = (g & 1) ? hi >> 8 : __funnelshift_r(lo, hi, 24);
+            const uint2 mine = steps.info[2 * st + (lane >> 4)];
+            const int j0 = (int)mine.y;
+            // key `lane`: the logit's factor, log2 of the value's and its reciprocal; one without a page
+            // weighs nothing, and neither its records nor an infinite factor reach a sum
+            {
+                const float2 fk = *reinterpret_cast<const float2 *>(rec + 14 * lane + 12),
+                             fv = *reinterpret_cast<const float2 *>(vrec + 14 * lane + 12);
+                float gv = __fmul_rn(fv.x, fv.y);
+                gv = gv < kTiny ? kTiny : gv;
+                float4 x = make_float4(__fmul_rn(__fmul_rn(fk.x, fk.y), coef), lg2(gv), rcp(gv), 0.0f);
+                if (!(mine.x >> (lane & 15) & 1u)) x = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+                factor[lane] = x;
             }
             __syncwarp();
-            ++steps.used;
-            request();
 
-            float S[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[n][e] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const Pair<kWide> a0 = lookup<kWide>(table, column, field(ka, 12 * j)),
-                                  a1 = lookup<kWide>(table, column, field(kb, 12 * j)),
-                                  a2 = lookup<kWide>(table, column, field(ka, 12 * j + 6)),
-                                  a3 = lookup<kWide>(table, column, field(kb, 12 * j + 6));
-#pragma unroll
-                for (int n = 0; n < NT; ++n) product<NT, kWide>(S[n], a0, a1, a2, a3, qh[n][j], ql[n][kWide ? j : 0]);
-            }
-            // s + log2 g and 1 / g of keys g, g + 8
-            const float f[2] = {__fmul_rn(__fmul_rn(fa.x, fa.y), coef), __fmul_rn(__fmul_rn(fb.x, fb.y), coef)};
-            float lg[2], inv[2];
+            float S[2][NT][4], live[2][NT][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float gv = x ? __fmul_rn(gb.x, gb.y) : __fmul_rn(ga.x, ga.y);
-                gv = gv < kTiny ? kTiny : gv;
-                lg[x] = lg2(gv), inv[x] = rcp(gv);
+                // keys g and g + 8 of the piece: words 3 t .. 3 t + 2 of the indices
+                uint32_t ka[3], kb[3];
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    ka[i] = rec[14 * (kPiece * x + g) + 3 * t + i], kb[i] = rec[14 * (kPiece * x + g + 8) + 3 * t + i];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[x][n][e] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const Pair<kWide> a0 = lookup<kWide>(table, column, field(ka, 12 * j)),
+                                      a1 = lookup<kWide>(table, column, field(kb, 12 * j)),
+                                      a2 = lookup<kWide>(table, column, field(ka, 12 * j + 6)),
+                                      a3 = lookup<kWide>(table, column, field(kb, 12 * j + 6));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) product<NT, kWide>(S[x][n], a0, a1, a2, a3, qh[n][j], ql[n][kWide ? j : 0]);
+                }
+                const float4 fa = factor[kPiece * x + g], fb = factor[kPiece * x + g + 8];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        S[x][n][e] = __fmaf_rn(S[x][n][e], e < 2 ? fa.x : fb.x, e < 2 ? fa.y : fb.y);
+                        live[x][n][e] = e < 2 ? fa.z : fb.z;
+                    }
             }
-            // 0 where the weight is masked: an infinite or NaN factor must not reach the row's sum
-            float live[NT][4];
-            const bool whole = valid == 0xffffu && j0 + kSub <= p_lo + 1 &&
-                               (a.window == 0 || j0 > p_hi - a.window || j0 + kSub <= a.sinks);
+            if (!(j0 + kSub <= p_lo + 1 && (a.window == 0 || j0 > p_hi - a.window || j0 + kSub <= a.sinks))) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = j0 + kPiece * x + g + 8 * (e >> 1), pos = p[n][e & 1];
+                            const bool on = j <= pos && (a.window == 0 || j > pos - a.window || j < a.sinks);
+                            if (!on) S[x][n][e] = -INFINITY, live[x][n][e] = 0.0f;
+                        }
+            }
             bool raise = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int x = e >> 1;
-                    S[n][e] = __fmaf_rn(S[n][e], f[x], lg[x]);
-                    live[n][e] = inv[x];
-                    if (!whole) {
-                        const int key = g + 8 * x, j = j0 + key, pos = p[n][e & 1];
-                        const bool on = ((valid >> key) & 1u) && j <= pos &&
-                                        (a.window == 0 || j > pos - a.window || j < a.sinks);
-                        if (!on) S[n][e] = -INFINITY, live[n][e] = 0.0f;
-                    }
-                    raise |= S[n][e] > __fadd_rn(M[n][e & 1], kLazy);
+                for (int e = 0; e < 2; ++e) {
+                    const float m = max3(fmaxf(S[0][n][e], S[0][n][e + 2]), S[1][n][e], S[1][n][e + 2]);
+                    raise |= m > __fadd_rn(M[n][e], kLazy);
                 }
             if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -440,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
                     float alpha[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = fmaxf(S[n][e], S[n][e + 2]);
+                        float m = max3(fmaxf(S[0][n][e], S[0][n][e + 2]), S[1][n][e], S[1][n][e + 2]);
 #pragma unroll
                         for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                         m = fmaxf(m, M[n][e]);
@@ -449,48 +475,65 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
                         l[n][e] = __fmul_rn(l[n][e], alpha[e]);
                     }
 #pragma unroll
-                    for (int i2 = 0; i2 < 8; ++i2)
+                    for (int i = 0; i < 8; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[n][i2][e] = __fmul_rn(acc[n][i2][e], alpha[e & 1]);
+                        for (int e = 0; e < 4; ++e) acc[n][i][e] = __fmul_rn(acc[n][i][e], alpha[e & 1]);
                 }
             }
-            uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float e4[4];
+            for (int x = 0; x < 2; ++x) {
+                uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    e4[e] = ex2(__fsub_rn(S[n][e], __fsub_rn(M[n][e & 1], kLift)));
-                    l[n][e & 1] = __fmaf_rn(e4[e], live[n][e], l[n][e & 1]);
+                for (int n = 0; n < NT; ++n) {
+                    float w4[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w4[e] = ex2(__fsub_rn(S[x][n][e], __fsub_rn(M[n][e & 1], kLift)));
+                        l[n][e & 1] = __fmaf_rn(w4[e], live[x][n][e], l[n][e & 1]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t hi = pack_half2(w4[2 * i], w4[2 * i + 1]);
+                        ph[n][i] = transpose8x8(hi);
+                        pl[n][i] = kWide ? transpose8x8(residue_half2(w4[2 * i], w4[2 * i + 1], hi)) : 0u;
+                    }
                 }
+                // values of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: coordinates 16 g .. 16 g + 15, bits 48 g
+                // on, as two groups of 24 bits
+                uint32_t v[4][2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t hi = pack_half2(e4[2 * x], e4[2 * x + 1]);
-                    ph[n][x] = transpose8x8(hi);
-                    pl[n][x] = kWide ? transpose8x8(residue_half2(e4[2 * x], e4[2 * x + 1], hi)) : 0u;
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t *const at = vrec + 14 * (kPiece * x + 2 * t + (i & 1) + 8 * (i >> 1)) + (3 * g >> 1);
+                    const uint32_t lo = at[0], hi = at[1];
+                    v[i][0] = __funnelshift_r(lo, hi, 16 * (g & 1));
+                    v[i][1] = __funnelshift_r((g & 1) ? hi : lo, hi, (g & 1) ? 8 : 24);
+                }
+                // per group: pairs (key 2 t, key 2 t + 1) of one coordinate, even ones and odd ones
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    constexpr uint32_t even = 0x1c71c7u, odd = even << 3;
+                    const uint32_t e0[1] = {(v[0][h] & even) | ((v[1][h] << 3) & odd)},
+                                   o0[1] = {((v[0][h] >> 3) & even) | (v[1][h] & odd)},
+                                   e1[1] = {(v[2][h] & even) | ((v[3][h] << 3) & odd)},
+                                   o1[1] = {((v[2][h] >> 3) & even) | (v[3][h] & odd)};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const Pair<kWide> a0 = lookup<kWide>(table, column, field(e0, 6 * c)),
+                                          a1 = lookup<kWide>(table, column, field(o0, 6 * c)),
+                                          a2 = lookup<kWide>(table, column, field(e1, 6 * c)),
+                                          a3 = lookup<kWide>(table, column, field(o1, 6 * c));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) product<NT, kWide>(acc[n][4 * h + c], a0, a1, a2, a3, ph[n], pl[n]);
+                    }
                 }
             }
-            // per 8 coordinates: pairs (key 2 t, key 2 t + 1) of one coordinate, even ones and odd ones
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t even = 0x1c71c7u, odd = even << 3;
-                const uint32_t e0[1] = {(v[0][h] & even) | ((v[1][h] << 3) & odd)},
-                               o0[1] = {((v[0][h] >> 3) & even) | (v[1][h] & odd)},
-                               e1[1] = {(v[2][h] & even) | ((v[3][h] << 3) & odd)},
-                               o1[1] = {((v[2][h] >> 3) & even) | (v[3][h] & odd)};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const Pair<kWide> a0 = lookup<kWide>(table, column, field(e0, 6 * c)),
-                                      a1 = lookup<kWide>(table, column, field(o0, 6 * c)),
-                                      a2 = lookup<kWide>(table, column, field(e1, 6 * c)),
-                                      a3 = lookup<kWide>(table, column, field(o1, 6 * c));
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) product<NT, kWide>(acc[n][4 * h + c], a0, a1, a2, a3, ph[n], pl[n]);
-                }
-            }
+            __syncwarp();
+            ++steps.used;
+            steps.request(a, w, warp, lane);
         }
 
-        // join the warps: row r by warp r % 8
+        // join the warps: row r by warp r % kWarps. No copy is in flight (unless a wait ran out), so a
+        // warp's sums lie where its stages were
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -500,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
                 for (int o = 4; o <= 16; o <<= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
                 const int r = 8 * n + 2 * t + e;
                 if (g == 0) *reinterpret_cast<float2 *>(stat + 2 * (warp * R + r)) = make_float2(M[n][e], x);
-                float *const to = merge + (warp * R + r) * 132 + 16 * g;
+                float *const to = reinterpret_cast<float *>(steps.stage) + r * 132 + 16 * g;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<float2 *>(to + 2 * i) = make_float2(acc[n][i][e], acc[n][i][e + 2]);
@@ -514,8 +557,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
             *cut = c;
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = 8 * n + warp;
+        for (int n = 0; n < R / kWarps; ++n) {
+            const int r = kWarps * n + warp;
             if (r0 + r >= rows) continue;
             float m = -FLT_MAX, sum = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -524,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
             for (int x = 0; x < kWarps; ++x) {
                 const float2 ml = *reinterpret_cast<const float2 *>(stat + 2 * (x * R + r));
                 const float f = ex2(__fsub_rn(ml.x, m));
-                const float4 o = *reinterpret_cast<const float4 *>(merge + (x * R + r) * 132 + 4 * lane);
+                const float4 o = *reinterpret_cast<const float4 *>(smem + L::kOffStage + x * L::kWarpBytes + r * 528 + 16 * lane);
                 sum = __fmaf_rn(ml.y, f, sum);
                 v[0] = __fmaf_rn(o.x, f, v[0]);
                 v[1] = __fmaf_rn(o.y, f, v[1]);
@@ -541,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 2 : 1) rows_kern
                 if (lane == 0) slot[R * 128 + r] = sum == 0.0f ? -INFINITY : m, slot[R * 129 + r] = sum;
             }
         }
+        fence_proxy_async_smem();  // the stages are copied into again
         __syncthreads();
     }
     // no copy outlives the CTA
@@ -562,7 +606,7 @@ unsigned int read_and_clear_fault() {
     return v;
 }
 
-constexpr int kParts = 2 * kSms;
+constexpr int kParts = 4 * kSms;
 
 template <int NT, bool kWide>
 wq_status run_rows(const Args &a, cudaStream_t s) {
