@@ -44,7 +44,6 @@ static_assert(kSub == 2 * kPiece, "two pieces a step, a lane per key");
 constexpr int kStages = 3;
 constexpr int kPieceBytes = kPiece * tq3_cache::kRec;
 constexpr int kStageBytes = 4 * kPieceBytes;  // a step's key records, then its value records
-constexpr uint32_t kMaxPolls = 1u << 24;
 constexpr float kLazy = 8.0f;   // M_i is raised past this margin (log2 units)
 constexpr float kLift = 6.0f;   // weights are at most 2^(kLazy + kLift) < 65504, so 2^-20 of the largest is still normal
 constexpr float kTiny = 0x1p-100f;  // least g_j: a zero vector weighs 2^-100 instead
@@ -64,12 +63,11 @@ struct Layout {
     static constexpr int kOffQ = kOffFactor + kWarps * kSub * 16;
     static constexpr int kOffStat = kOffQ + (kWide ? 2 : 1) * kQ * 2;  // per warp and row: M, l
     static constexpr int kOffTop = kOffStat + kWarps * kRows * 8;      // per row: max |q~|
-    static constexpr int kOffBar = kOffTop + kRows * 4;
-    static constexpr int kOffValid = kOffBar + kWarps * kStages * 8;  // per warp, stage and piece
-    static constexpr int kOffScratch = kOffValid + kWarps * kStages * 16;
-    static constexpr int kBytes = kOffScratch + (kWarps + 2) * 8;
+    static constexpr int kOffInfo = kOffTop + kRows * 4;               // per warp and stage
+    static constexpr int kOffScratch = kOffInfo + kWarps * kStages * 8;
+    static constexpr int kBytes = kOffScratch + (kWarps + 4) * 8;
     static_assert(kRows * 132 * 4 <= kWarpBytes, "a warp's sums fit its stages");
-    static_assert(kOffQ % 16 == 0 && kOffBar % 8 == 0 && kOffScratch % 8 == 0 && kBytes <= 227 * 1024, "layout");
+    static_assert(kOffQ % 16 == 0 && kOffInfo % 8 == 0 && kOffScratch % 8 == 0 && kBytes <= 227 * 1024, "layout");
 };
 
 __device__ __forceinline__ float lg2(float x) {
@@ -142,31 +140,30 @@ __device__ __forceinline__ void product(float (&d)[4], const Pair<kWide> &a0, co
     }
 }
 
-// Whether the phase has completed, within the bounds of mbar_wait_bounded; the first poll is cheap.
-__device__ __forceinline__ bool wait_copy(uint64_t *bar, uint32_t phase) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(phase)
-                 : "memory");
-    return ok || mbar_wait_bounded(bar, phase, kMaxPolls);
+__device__ __forceinline__ void cp_async16(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ int64_t shfl64(int64_t v, int from) {
+    const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)v, from), hi = __shfl_sync(0xffffffffu, (uint32_t)((uint64_t)v >> 32), from);
+    return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-// A warp's stream of 32-key steps through its stages. Pieces are requested 32 at a time (16 steps), a
-// lane each: its lane works out where the piece lies and later starts its copies.
+// A warp's stream of 32-key steps through its stages: one group of asynchronous copies a step. Pieces
+// are looked up 32 at a time (16 steps), a lane each.
 struct Steps {
-    unsigned char *stage;  // kStages of kStageBytes
-    uint64_t *bar;         // per stage, two arrivals: a piece each
-    uint2 *info;           // per stage and piece: which of its keys have a page; the step's first key
+    uint32_t stage;  // shared address of kStages of kStageBytes
+    uint2 *info;     // per stage: the keys that have a page, the step's first key
     uint32_t issued, used;
-    bool dead;
     // of the segment
     int b, head, take, last, from, until;
     // of the 32 pieces in hand: steps that are still to be requested (bit 2 i), and this lane's piece
     int base;
     uint32_t todo;
     int j;
-    int32_t page;  // its page, -1 where no row sees the piece, -2 where the page is outside the pool
+    int64_t at;  // byte offset in its pool, -1 without a page
 
     __device__ __forceinline__ bool seen(int j0, int n) const { return j0 <= last && (j0 + n > from || j0 < until); }
 
@@ -175,96 +172,80 @@ struct Steps {
         b = w.b, head = w.head, take = w.take(), last = p_hi, from = w.span.from, until = w.span.until;
         base = 0, todo = 0;
     }
+    // The offset of key j0's page and place in it, or -1 with the fault bit set.
+    __device__ __forceinline__ int64_t locate(const Args &a, int j0) const {
+        const int32_t page = __ldg(a.table + b * a.pages_per_seq + (j0 >> a.pools.shift));
+        if (page >= 0 && page < a.pools.n_pages)
+            return tq3_cache::record_at(a.pools, page, head, j0 & ((1 << a.pools.shift) - 1));
+        atomicOr(&g_fault, tq3::kFaultPoolIndex);
+        return -1;
+    }
     template <class W>
     __device__ __forceinline__ void gather(const Args &a, const W &w, int warp, int lane) {
         const int i = base + (lane >> 1);
         bool need = false;
-        page = -1;
+        at = -1;
         j = 0;
         if (i < take) {
             j = w.span.tile(w.tile + i) * kTileKeys + warp * kSub + (lane & 1) * kPiece;
             need = seen(j, kPiece);
-            if (need && a.pools.shift >= 4) {
-                page = __ldg(a.table + b * a.pages_per_seq + (j >> a.pools.shift));
-                if (page < 0 || page >= a.pools.n_pages) {
-                    atomicOr(&g_fault, tq3::kFaultPoolIndex);
-                    page = -2;
-                }
-            }
+            if (need && a.pools.shift >= 4) at = locate(a, j);
         }
         const uint32_t m = __ballot_sync(0xffffffffu, need);
         todo = (m | m >> 1) & 0x55555555u;
         base += 16;
     }
+    // Fills the free stages. Every call commits as many groups as make kStages - 1 of them follow the
+    // step that is used next, empty ones at the end of a segment.
     template <class W>
-    __device__ __forceinline__ void request(const Args &a, const W &w, int warp, int lane) {
-        while (issued - used < kStages) {
-            if (todo == 0) {
-                if (base >= take || dead) return;
-                gather(a, w, warp, lane);
-                continue;
+    __device__ __forceinline__ void request(const Args &a, const W &w, int warp, int lane, int steps) {
+        for (int k = 0; k < steps; ++k) {
+            while (todo == 0 && base < take) gather(a, w, warp, lane);
+            if (todo) {
+                const int p = __ffs(todo) - 1, st = issued % kStages;
+                todo &= todo - 1;
+                const int j0 = __shfl_sync(0xffffffffu, j, p);
+                const uint32_t keys = a.pools.shift >= 4 ? copy_pieces(a, st, p, lane) : copy_small(a, st, j0, lane);
+                if (lane == 0) info[st] = make_uint2(keys, (uint32_t)j0);
+                ++issued;
             }
-            const int at = __ffs(todo) - 1, st = issued % kStages;
-            todo &= todo - 1;
-            if (a.pools.shift >= 4) {
-                if ((lane & ~1) == at) copy_piece(a, st, lane & 1);
-            } else {
-                copy_small(a, st, __shfl_sync(0xffffffffu, j, at), lane);
-            }
-            ++issued;
+            asm volatile("cp.async.commit_group;" ::: "memory");
         }
     }
-    // 16 keys of one page, by the lane that holds it.
-    __device__ __forceinline__ void copy_piece(const Args &a, int st, int half) const {
-        info[2 * st + half] = make_uint2(page >= 0 ? 0xffffu : 0u, (uint32_t)(j - half * kPiece));
-        if (page >= 0) {
-            unsigned char *const dst = stage + st * kStageBytes + half * kPieceBytes;
-            const int64_t at = tq3_cache::record_at(a.pools, page, head, j & ((1 << a.pools.shift) - 1));
-            mbar_expect_tx(bar + st, 2 * kPieceBytes);
-            bulk_load(dst, a.pools.k + at, kPieceBytes, bar + st);
-            bulk_load(dst + 2 * kPieceBytes, a.pools.v + at, kPieceBytes, bar + st);
-        } else {
-            mbar_arrive(bar + st);
-        }
+    // Two pieces of 16 keys, each within a page, in 16-byte chunks: 56 of each piece in either pool.
+    // Shared: key pieces 0 and 1, value pieces 0 and 1.
+    __device__ __forceinline__ uint32_t copy_pieces(const Args &a, int st, int p, int lane) const {
+        const int64_t a0 = shfl64(at, p), a1 = shfl64(at, p + 1);
+        const uint32_t b0 = a0 >= 0 ? 16 : 0, b1 = a1 >= 0 ? 16 : 0;  // nothing is read for 0 bytes
+        const uint8_t *const k0 = a.pools.k + (a0 >= 0 ? a0 : 0) + 16 * lane, *const k1 = a.pools.k + (a1 >= 0 ? a1 : 0) + 16 * lane;
+        const uint8_t *const v0 = a.pools.v + (a0 >= 0 ? a0 : 0) + 16 * lane, *const v1 = a.pools.v + (a1 >= 0 ? a1 : 0) + 16 * lane;
+        const uint32_t dst = stage + st * kStageBytes + 16 * lane;
+        cp_async16(dst, k0, b0);
+        cp_async16(dst + 512, lane < 24 ? k0 + 512 : k1 + 512 - kPieceBytes, lane < 24 ? b0 : b1);
+        cp_async16(dst + 1024, k1 + 1024 - kPieceBytes, b1);
+        cp_async16(dst + 1536, lane < 16 ? k1 + 1536 - kPieceBytes : v0 + 1536 - 2 * kPieceBytes, lane < 16 ? b1 : b0);
+        cp_async16(dst + 2048, v0 + 2048 - 2 * kPieceBytes, b0);
+        cp_async16(dst + 2560, lane < 8 ? v0 + 2560 - 2 * kPieceBytes : v1 + 2560 - 3 * kPieceBytes, lane < 8 ? b0 : b1);
+        cp_async16(dst + 3072, v1 + 3072 - 3 * kPieceBytes, b1);
+        return (a0 >= 0 ? 0xffffu : 0u) | (a1 >= 0 ? 0xffff0000u : 0u);
     }
-    // 32 keys in pages of 1 to 8 places, a page a lane. A record alone is not a multiple of 16 bytes, so
-    // pages of one place are copied by the lanes themselves.
-    __device__ __forceinline__ void copy_small(const Args &a, int st, int j0, int lane) const {
-        const tq3_cache::Pools &pools = a.pools;
-        const int shift = pools.shift, size = 1 << shift, jp = j0 + (lane << shift);
-        const bool need = lane < (kSub >> shift) && seen(jp, size);
-        const int32_t p = need ? __ldg(a.table + b * a.pages_per_seq + (jp >> shift)) : -1;
-        const bool ok = need && p >= 0 && p < pools.n_pages;
-        if (need && !ok) atomicOr(&g_fault, tq3::kFaultPoolIndex);
-        const uint32_t keys = __reduce_or_sync(0xffffffffu, ok ? ((1u << size) - 1u) << (lane << shift) : 0u);
-        const int64_t at = ok ? tq3_cache::record_at(pools, p, head, 0) : 0;
-        unsigned char *const dst = stage + st * kStageBytes + (lane << shift) * tq3_cache::kRec;
-        if (lane < 2) info[2 * st + lane] = make_uint2(keys >> (16 * lane) & 0xffffu, (uint32_t)j0);
-        if (shift == 0) {
-            if (ok)
-#pragma unroll
-                for (int i = 0; i < 7; ++i) {
-                    reinterpret_cast<uint2 *>(dst)[i] = __ldg(reinterpret_cast<const uint2 *>(pools.k + at) + i);
-                    reinterpret_cast<uint2 *>(dst + 2 * kPieceBytes)[i] = __ldg(reinterpret_cast<const uint2 *>(pools.v + at) + i);
-                }
-            __syncwarp();
-            if (lane < 2) mbar_arrive(bar + st);
-        } else {
-            const uint32_t bytes = tq3_cache::kRec << shift;
-            if (lane < 2) mbar_expect_tx(bar + st, __popc(keys >> (16 * lane) & 0xffffu) * 2 * tq3_cache::kRec);
-            __syncwarp();
-            if (ok) {
-                bulk_load(dst, pools.k + at, bytes, bar + st);
-                bulk_load(dst + 2 * kPieceBytes, pools.v + at, bytes, bar + st);
-            }
+    // 32 keys in pages of 1 to 8 places, a page a lane, in 8-byte chunks (a lone record is not a multiple
+    // of 16 bytes).
+    __device__ __forceinline__ uint32_t copy_small(const Args &a, int st, int j0, int lane) const {
+        const int shift = a.pools.shift, size = 1 << shift, jp = j0 + (lane << shift);
+        const int64_t mine = lane < (kSub >> shift) && seen(jp, size) ? locate(a, jp) : -1;
+#pragma unroll 1
+        for (int i = 0; i < kStageBytes / 256; ++i) {
+            const int c = 32 * i + lane, tensor = c / (7 * kSub), r = c % (7 * kSub) / 7, word = c % 7;
+            const int64_t from_at = shfl64(mine, r >> shift);
+            const uint8_t *const src = (tensor ? a.pools.v : a.pools.k) +
+                                       (from_at >= 0 ? from_at + (r & (size - 1)) * tq3_cache::kRec + 8 * word : 0);
+            cp_async8(stage + st * kStageBytes + 8 * c, src, from_at >= 0 ? 8 : 0);
         }
-    }
-    __device__ __forceinline__ bool arrived(int lane) {
-        const bool ok = __all_sync(0xffffffffu, wait_copy(bar + used % kStages, (used / kStages) & 1u));
-        if (!ok && lane == 0) atomicOr(&g_fault, 128u);
-        return ok;
+        return __reduce_or_sync(0xffffffffu, mine >= 0 ? ((1u << size) - 1u) << (lane << shift) : 0u);
     }
 };
+constexpr int kAhead = kStages - 1;  // steps requested beyond the one in use
 
 template <int NT, bool kWide>
 __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kernel(const __grid_constant__ Args a) {
@@ -292,15 +273,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
             reinterpret_cast<uint32_t *>(table)[i] = hi;
     }
     Steps steps;
-    steps.stage = smem + L::kOffStage + warp * L::kWarpBytes;
-    steps.bar = reinterpret_cast<uint64_t *>(smem + L::kOffBar) + warp * kStages;
-    steps.info = reinterpret_cast<uint2 *>(smem + L::kOffValid) + warp * kStages * 2;
+    unsigned char *const stages = smem + L::kOffStage + warp * L::kWarpBytes;
+    steps.stage = smem_u32(stages);
+    steps.info = reinterpret_cast<uint2 *>(smem + L::kOffInfo) + warp * kStages;
     steps.issued = steps.used = 0;
-    steps.dead = false;
-    if (lane == 0)
-        for (int i = 0; i < kStages; ++i) mbar_init(steps.bar + i, 2);
     Walk<R, kThreads> w;
-    w.start(a, reinterpret_cast<int64_t *>(smem + L::kOffScratch));
+    pdl_wait();  // what follows reads what earlier kernels wrote
+    const Line line = w.start(a, reinterpret_cast<int64_t *>(smem + L::kOffScratch));
+    pdl_trigger();
     Cut *const cut = reinterpret_cast<Cut *>(a.ws + (int64_t)blockIdx.x * kCutBytes);
     if (tid == 0) cut->cut = 0;
     if (blockIdx.x == 0)
@@ -314,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
         const int take = w.take();
 
         steps.begin(w, p_hi);
-        steps.request(a, w, warp, lane);
+        steps.request(a, w, warp, lane, kAhead);
 
         // q~ of the block's rows, scaled by the power of two that brings the largest to 2^13 .. 2^14
         float down;
@@ -376,6 +356,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
                 p[n][e] = r < rows ? before + r / a.group : -1;
             }
         }
+        // the first and the second three bytes of a lane's 48 bits in the two words that hold them
+        const uint32_t first = (g & 1) ? 0x5432u : 0x3210u, second = (g & 1) ? 0x7765u : 0x6543u;
         float acc[NT][8][4], M[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -388,14 +370,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
         }
 
         while (steps.used != steps.issued) {
-            if (steps.dead || !steps.arrived(lane)) {
-                steps.dead = true;
-                break;
-            }
+            steps.request(a, w, warp, lane, 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+            __syncwarp();
             const int st = steps.used % kStages;
-            const uint32_t *const rec = reinterpret_cast<const uint32_t *>(steps.stage + st * kStageBytes);
+            const uint32_t *const rec = reinterpret_cast<const uint32_t *>(stages + st * kStageBytes);
             const uint32_t *const vrec = rec + 14 * kSub;
-            const uint2 mine = steps.info[2 * st + (lane >> 4)];
+            const uint2 mine = steps.info[st];
             const int j0 = (int)mine.y;
             // key `lane`: the logit's factor, log2 of the value's and its reciprocal; one without a page
             // weighs nothing, and neither its records nor an infinite factor reach a sum
@@ -405,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
                 float gv = __fmul_rn(fv.x, fv.y);
                 gv = gv < kTiny ? kTiny : gv;
                 float4 x = make_float4(__fmul_rn(__fmul_rn(fk.x, fk.y), coef), lg2(gv), rcp(gv), 0.0f);
-                if (!(mine.x >> (lane & 15) & 1u)) x = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+                if (!(mine.x >> lane & 1u)) x = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
                 factor[lane] = x;
             }
             __syncwarp();
@@ -505,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t *const at = vrec + 14 * (kPiece * x + 2 * t + (i & 1) + 8 * (i >> 1)) + (3 * g >> 1);
                     const uint32_t lo = at[0], hi = at[1];
-                    v[i][0] = __funnelshift_r(lo, hi, 16 * (g & 1));
-                    v[i][1] = __funnelshift_r((g & 1) ? hi : lo, hi, (g & 1) ? 8 : 24);
+                    v[i][0] = __byte_perm(lo, hi, first);
+                    v[i][1] = __byte_perm(lo, hi, second);
                 }
                 // per group: pairs (key 2 t, key 2 t + 1) of one coordinate, even ones and odd ones
 #pragma unroll
@@ -527,13 +508,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
                     }
                 }
             }
-            __syncwarp();
+            __syncwarp();  // the stage and the factors are free
             ++steps.used;
-            steps.request(a, w, warp, lane);
         }
 
-        // join the warps: row r by warp r % kWarps. No copy is in flight (unless a wait ran out), so a
-        // warp's sums lie where its stages were
+        // join the warps: row r by warp r % kWarps. No copy is in flight, so a warp's sums lie where its
+        // stages were
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -543,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
                 for (int o = 4; o <= 16; o <<= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
                 const int r = 8 * n + 2 * t + e;
                 if (g == 0) *reinterpret_cast<float2 *>(stat + 2 * (warp * R + r)) = make_float2(M[n][e], x);
-                float *const to = reinterpret_cast<float *>(steps.stage) + r * 132 + 16 * g;
+                float *const to = reinterpret_cast<float *>(stages) + r * 132 + 16 * g;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<float2 *>(to + 2 * i) = make_float2(acc[n][i][e], acc[n][i][e + 2]);
@@ -553,7 +533,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
         float *const slot = slot_at<R>(a, gridDim.x, 2 * blockIdx.x + (w.tile == 0));
         if (!whole && w.tile == 0 && tid == 0) {
             Cut c;
-            c.total = w.total, c.end = w.at + w.segment(), c.cut = 1, c.seq = w.b, c.head = w.head, c.block = w.block;
+            c.cut = 1, c.n = line.part_of(w.at + w.segment() - 1) - (int)blockIdx.x + 1;
+            c.seq = w.b, c.head = w.head, c.block = w.block;
             *cut = c;
         }
 #pragma unroll
@@ -584,19 +565,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
                 if (lane == 0) slot[R * 128 + r] = sum == 0.0f ? -INFINITY : m, slot[R * 129 + r] = sum;
             }
         }
-        fence_proxy_async_smem();  // the stages are copied into again
         __syncthreads();
-    }
-    // no copy outlives the CTA
-    while (steps.used != steps.issued) {
-        mbar_wait_bounded(steps.bar + steps.used % kStages, (steps.used / kStages) & 1u, kMaxPolls);
-        ++steps.used;
     }
 }
 
 template <int R>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args a) {
-    merge_cut<R, kThreads>(a, gridDim.x);
+    pdl_wait();
+    merge_cut<R, kThreads>(a);
 }
 
 unsigned int read_and_clear_fault() {
@@ -608,12 +584,26 @@ unsigned int read_and_clear_fault() {
 
 constexpr int kParts = 4 * kSms;
 
+template <int R>
+void launch_join(const Args &a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kParts, R / kWarps);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, join_kernel<R>, a);
+}
+
 template <int NT, bool kWide>
 wq_status run_rows(const Args &a, cudaStream_t s) {
     using L = Layout<NT, kWide>;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(rows_kernel<NT, kWide>), L::kBytes)) return WQ_ERR_CUDA;
-    rows_kernel<NT, kWide><<<kParts, kThreads, L::kBytes, s>>>(a);
-    join_kernel<L::kRows><<<kParts, kThreads, 0, s>>>(a);
+    launch_pdl(rows_kernel<NT, kWide>, kParts, kThreads, L::kBytes, s, a);
+    launch_join<L::kRows>(a, s);
     return launch_status();
 }
 

@@ -8,7 +8,7 @@
 // is cut into equal parts, one per CTA, whatever the sequences' lengths. Each CTA finds its part from
 // q_start and kv_len alone. A segment inside one part is finished there; one that is cut leaves a
 // partial result per part (rows normalised by their own sums, with the maxima and sums), which
-// merge_kernel joins in the order of the parts: the result does not depend on timing.
+// the join kernel joins in the order of the parts: the result does not depend on timing.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -100,13 +100,29 @@ __device__ __forceinline__ int64_t tiles_of_head(const Args &a, const Seq &s) {
     return n;
 }
 
-// Header of a part whose last segment is cut, written by that part's CTA for merge_kernel.
-struct Cut {
-    int64_t total;     // tiles of the whole launch
-    int64_t end;       // where on the line the segment ends
-    int cut, seq, head, block;
+// Part c of n is [begin(c), begin(c + 1)), the first total % n parts one tile longer. There are as many
+// parts as CTAs, or one per tile where there are fewer tiles: none is empty.
+struct Line {
+    int64_t each;
+    int rest, parts;
+    __device__ __forceinline__ Line(int64_t total, int ctas) {
+        parts = total < ctas ? (int)total : ctas;
+        each = parts ? total / parts : 0;
+        rest = parts ? (int)(total - each * parts) : 0;
+    }
+    __device__ __forceinline__ int64_t begin(int c) const { return each * c + min(c, rest); }
+    __device__ __forceinline__ int part_of(int64_t at) const {
+        const int64_t longer = (each + 1) * rest;
+        return (int)(at < longer ? at / (each + 1) : rest + (at - longer) / each);
+    }
 };
-constexpr int kCutBytes = 64;
+
+// Header of a part, for the join: whether its last segment goes on in the next parts, how many parts it
+// is in, and which one it is.
+struct Cut {
+    int cut, n, seq, head, block;
+};
+constexpr int kCutBytes = 32;
 
 template <int R>
 __host__ __device__ constexpr int64_t slot_floats() {
@@ -114,56 +130,59 @@ __host__ __device__ constexpr int64_t slot_floats() {
 }
 // Slot 2c: the segment that part c continues; 2c + 1: the one that it begins and does not finish.
 template <int R>
-__device__ __forceinline__ float *slot_at(const Args &a, int parts, int i) {
-    return reinterpret_cast<float *>(a.ws + (int64_t)parts * kCutBytes) + i * slot_floats<R>();
+__device__ __forceinline__ float *slot_at(const Args &a, int ctas, int i) {
+    return reinterpret_cast<float *>(a.ws + (int64_t)ctas * kCutBytes) + i * slot_floats<R>();
 }
 template <int R>
-constexpr int64_t workspace_bytes(int64_t parts) {
-    return parts * (kCutBytes + 2 * slot_floats<R>() * 4);
+constexpr int64_t workspace_bytes(int64_t ctas) {
+    return ctas * (kCutBytes + 2 * slot_floats<R>() * 4);
 }
-
-__device__ __forceinline__ int64_t part_begin(int64_t total, int part, int parts) { return total * part / parts; }
 
 // Walks this CTA's part of the line. All threads of the CTA hold the same state.
 template <int R, int kThreads>
 struct Walk {
-    int64_t total, at, end;  // on the line
+    int64_t at, end;  // on the line
     int b, head, block, blocks, tile;  // tile: the first one of the segment that is this CTA's
     Seq seq;
     Span span;
 
-    // `scratch`: kThreads / 32 + 2 int64 in shared memory.
-    __device__ __forceinline__ void start(const Args &a, int64_t *scratch) {
+    // `scratch`: kThreads / 32 + 4 int64 in shared memory. Returns the line.
+    __device__ __forceinline__ Line start(const Args &a, int64_t *scratch) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         constexpr int kWarps = kThreads / 32;
-        int64_t mine = 0, first = 0;
-        for (int i = tid; i < a.batch; i += kThreads) {
-            const int64_t c = tiles_of_head<R>(a, load_seq(a, i)) * a.pools.heads;
-            if (i == tid) first = c;
-            mine += c;
+        // the tiles of all sequences, kThreads of them at a time
+        int64_t total = 0;
+        for (int base = 0; base < a.batch; base += kThreads) {
+            const int i = base + tid;
+            int64_t c = i < a.batch ? tiles_of_head<R>(a, load_seq(a, i)) * a.pools.heads : 0;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+            if (base) __syncthreads();
+            if (lane == 0) scratch[warp] = c;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) total += scratch[w];
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        if (lane == 0) scratch[warp] = mine;
-        __syncthreads();
-        total = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) total += scratch[w];
-        at = part_begin(total, blockIdx.x, gridDim.x);
-        end = part_begin(total, blockIdx.x + 1, gridDim.x);
-        __syncthreads();
-        if (at >= end) return;
-        // the sequence that holds `at`, by a prefix sum over kThreads sequences at a time
+        const Line line(total, gridDim.x);
+        at = end = 0;
+        if ((int)blockIdx.x >= line.parts) return line;
+        at = line.begin(blockIdx.x);
+        end = line.begin(blockIdx.x + 1);
+        // the sequence that holds `at`: prefix sums
         int64_t before = 0;
         for (int base = 0;; base += kThreads) {
             const int i = base + tid;
-            const int64_t c = base == 0 ? first : i < a.batch ? tiles_of_head<R>(a, load_seq(a, i)) * a.pools.heads : 0;
+            Seq s;
+            s.start = s.new_tokens = s.keys = 0;
+            if (i < a.batch) s = load_seq(a, i);
+            const int64_t c = i < a.batch ? tiles_of_head<R>(a, s) * a.pools.heads : 0;
             int64_t sum = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += v;
             }
+            __syncthreads();
             if (lane == 31) scratch[warp] = sum;
             __syncthreads();
             int64_t lead = before;
@@ -173,14 +192,18 @@ struct Walk {
             if (at >= lead + sum - c && at < lead + sum) {
                 scratch[kWarps] = i;
                 scratch[kWarps + 1] = at - (lead + sum - c);
+                scratch[kWarps + 2] = (int64_t)s.start << 32 | s.new_tokens;
+                scratch[kWarps + 3] = s.keys;
             }
-            __syncthreads();
             before = all;
             if (at < all) break;
         }
+        __syncthreads();
         b = (int)scratch[kWarps];
         int64_t off = scratch[kWarps + 1];
-        seq = load_seq(a, b);
+        seq.start = (int)(scratch[kWarps + 2] >> 32);
+        seq.new_tokens = (int)scratch[kWarps + 2];
+        seq.keys = (int)scratch[kWarps + 3];
         blocks = blocks_of<R>(a, seq);
         const int64_t per_head = tiles_of_head<R>(a, seq);
         head = (int)(off / per_head);
@@ -193,7 +216,7 @@ struct Walk {
             off -= n;
         }
         tile = (int)off;
-        __syncthreads();
+        return line;
     }
     __device__ __forceinline__ bool done() const { return at >= end; }
     __device__ __forceinline__ int segment() const { return max(1, span.n); }
@@ -282,46 +305,45 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-// Joins the partial results of the segments that parts leave cut (one CTA per part; kThreads / 32
-// warps, a row each).
+// Joins the partial results of the segments that parts leave cut: CTA (x, y) rows y * kThreads / 32 on of
+// part x's, a warp a row.
 template <int R, int kThreads>
-__device__ __forceinline__ void merge_cut(const Args &a, int parts) {
-    const int part = blockIdx.x, lane = threadIdx.x & 31;
+__device__ __forceinline__ void merge_cut(const Args &a) {
+    const int part = blockIdx.x, ctas = gridDim.x, lane = threadIdx.x & 31;
     const Cut c = *reinterpret_cast<const Cut *>(a.ws + (int64_t)part * kCutBytes);
     if (!c.cut) return;
     const Seq s = load_seq(a, c.seq);
-    const int rows = min(R, s.new_tokens * a.group - c.block * R);
-    // parts after this one up to the segment's end; an empty part has no slot
-    int last = part + 1;
-    while (last < parts && part_begin(c.total, last, parts) < c.end) ++last;
-    for (int r = threadIdx.x >> 5; r < rows; r += kThreads / 32) {
-        float top = -INFINITY;
-        for (int p = part + lane; p < last; p += 32) {
-            if (p > part && part_begin(c.total, p, parts) == part_begin(c.total, p + 1, parts)) continue;
-            top = fmaxf(top, slot_at<R>(a, parts, 2 * p + (p == part))[R * 128 + r]);
-        }
+    const int r = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5), row = c.block * R + r;
+    if (row >= s.new_tokens * a.group) return;
+    const float *const slots = slot_at<R>(a, ctas, 2 * part);  // the part's own one is its second
+    auto slot = [&](int i) { return slots + (i == 0 ? 1 : 2 * i) * slot_floats<R>(); };
+    float top = -INFINITY;
+    for (int i = lane; i < c.n; i += 32) top = fmaxf(top, slot(i)[R * 128 + r]);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
-        if (top != -INFINITY)
-            for (int p = part; p < last; ++p) {
-                if (p > part && part_begin(c.total, p, parts) == part_begin(c.total, p + 1, parts)) continue;
-                const float *const slot = slot_at<R>(a, parts, 2 * p + (p == part));
-                const float w = __fmul_rn(slot[R * 129 + r], ex2(__fsub_rn(slot[R * 128 + r], top)));
-                const float4 x = *reinterpret_cast<const float4 *>(slot + r * 128 + 4 * lane);
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sum = 0.0f;
+    if (top != -INFINITY)
+        for (int i0 = 0; i0 < c.n; i0 += 32) {
+            const int n = min(32, c.n - i0);
+            const float w_mine = lane < n ? __fmul_rn(slot(i0 + lane)[R * 129 + r], ex2(__fsub_rn(slot(i0 + lane)[R * 128 + r], top)))
+                                          : 0.0f;
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float w = __shfl_sync(0xffffffffu, w_mine, i);
+                const float4 x = *reinterpret_cast<const float4 *>(slot(i0 + i) + r * 128 + 4 * lane);
                 sum = __fadd_rn(sum, w);
                 v[0] = __fmaf_rn(w, x.x, v[0]);
                 v[1] = __fmaf_rn(w, x.y, v[1]);
                 v[2] = __fmaf_rn(w, x.z, v[2]);
                 v[3] = __fmaf_rn(w, x.w, v[3]);
             }
-        if (sum != 0.0f) {
-            const float f = __frcp_rn(sum);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], f);
         }
-        store_row(a, s, c.head, c.block * R + r, lane, v);
+    if (sum != 0.0f) {
+        const float f = __frcp_rn(sum);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], f);
     }
+    store_row(a, s, c.head, row, lane, v);
 }
 
 }  // namespace tq3_chunk
