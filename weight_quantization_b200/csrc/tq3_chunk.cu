@@ -35,6 +35,11 @@
 #include "tq3_common.cuh"
 
 namespace wq {
+namespace tq3_chunk_mma {  // tq3_chunk_mma.cu
+int64_t workspace();
+wq_status run(const tq3_chunk::Args &a, bool wide, cudaStream_t s);
+unsigned int read_and_clear_fault();
+}  // namespace tq3_chunk_mma
 namespace tq3_chunk {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
     steps.issued = steps.used = 0;
     Walk<R, kThreads> w;
     pdl_wait();  // what follows reads what earlier kernels wrote
-    const Line line = w.start(a, reinterpret_cast<int64_t *>(smem + L::kOffScratch));
+    w.start(a, reinterpret_cast<int64_t *>(smem + L::kOffScratch));
     pdl_trigger();
     Cut *const cut = reinterpret_cast<Cut *>(a.ws + (int64_t)blockIdx.x * kCutBytes);
     if (tid == 0) cut->cut = 0;
@@ -531,12 +536,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
         __syncthreads();
         const bool whole = w.tile == 0 && take == w.segment();
         float *const slot = slot_at<R>(a, gridDim.x, 2 * blockIdx.x + (w.tile == 0));
-        if (!whole && w.tile == 0 && tid == 0) {
-            Cut c;
-            c.cut = 1, c.n = line.part_of(w.at + w.segment() - 1) - (int)blockIdx.x + 1;
-            c.seq = w.b, c.head = w.head, c.block = w.block;
-            *cut = c;
-        }
+        if (!whole && w.tile == 0 && tid == 0) *cut = w.cut_here();
 #pragma unroll
         for (int n = 0; n < R / kWarps; ++n) {
             const int r = kWarps * n + warp;
@@ -569,41 +569,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
     }
 }
 
-template <int R>
-__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Args a) {
-    pdl_wait();
-    merge_cut<R, kThreads>(a);
-}
-
 unsigned int read_and_clear_fault() {
     unsigned int v = 0, zero = 0;
     if (cudaMemcpyFromSymbol(&v, g_fault, sizeof v) != cudaSuccess) return 0x80000000u;
     if (v) cudaMemcpyToSymbol(g_fault, &zero, sizeof zero);
-    return v;
+    return v | tq3_chunk_mma::read_and_clear_fault();
 }
 
 constexpr int kParts = 4 * kSms;
-
-template <int R>
-void launch_join(const Args &a, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kParts, R / kWarps);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, join_kernel<R>, a);
-}
+constexpr int kFewRows = 8;  // rows per KV head of a sequence that the rows kernel serves
+inline int64_t rows_workspace() { return (workspace_bytes<8>(kParts) + 15) & ~int64_t(15); }
 
 template <int NT, bool kWide>
 wq_status run_rows(const Args &a, cudaStream_t s) {
     using L = Layout<NT, kWide>;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(rows_kernel<NT, kWide>), L::kBytes)) return WQ_ERR_CUDA;
     launch_pdl(rows_kernel<NT, kWide>, kParts, kThreads, L::kBytes, s, a);
-    launch_join<L::kRows>(a, s);
+    launch_join<L::kRows>(a, kParts, s);
     return launch_status();
 }
 
@@ -614,7 +596,7 @@ using namespace wq;
 
 extern "C" int64_t tq3_attention_chunk_workspace(int64_t max_q, int64_t group) {
     if (max_q < 0 || group < 1) return -1;
-    return tq3_chunk::workspace_bytes<8>(tq3_chunk::kParts);
+    return tq3_chunk::rows_workspace() + (max_q > tq3_chunk::kFewRows / group ? tq3_chunk_mma::workspace() : 0);
 }
 
 extern "C" wq_status tq3_attention_chunk(const void *q, int q_dtype, int64_t n_tokens, int64_t q_heads,
@@ -660,5 +642,11 @@ extern "C" wq_status tq3_attention_chunk(const void *q, int q_dtype, int64_t n_t
     a.ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool wide = !a.q_bf16 || !a.out_bf16;
-    return wide ? tq3_chunk::run_rows<1, true>(a, s) : tq3_chunk::run_rows<1, false>(a, s);
+    const bool few = max_q <= tq3_chunk::kFewRows / group;
+    if (!few) a.rows_to = tq3_chunk::kFewRows + 1;
+    const wq_status st = wide ? tq3_chunk::run_rows<1, true>(a, s) : tq3_chunk::run_rows<1, false>(a, s);
+    if (few || st != WQ_OK) return st;
+    a.rows_from = a.rows_to, a.rows_to = INT32_MAX;
+    a.ws += tq3_chunk::rows_workspace();
+    return tq3_chunk_mma::run(a, wide, s);
 }

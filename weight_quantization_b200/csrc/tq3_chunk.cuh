@@ -105,6 +105,7 @@ __device__ __forceinline__ int64_t tiles_of_head(const Args &a, const Seq &s) {
 struct Line {
     int64_t each;
     int rest, parts;
+    Line() = default;
     __device__ __forceinline__ Line(int64_t total, int ctas) {
         parts = total < ctas ? (int)total : ctas;
         each = parts ? total / parts : 0;
@@ -141,13 +142,14 @@ constexpr int64_t workspace_bytes(int64_t ctas) {
 // Walks this CTA's part of the line. All threads of the CTA hold the same state.
 template <int R, int kThreads>
 struct Walk {
+    Line line;
     int64_t at, end;  // on the line
     int b, head, block, blocks, tile;  // tile: the first one of the segment that is this CTA's
     Seq seq;
     Span span;
 
-    // `scratch`: kThreads / 32 + 4 int64 in shared memory. Returns the line.
-    __device__ __forceinline__ Line start(const Args &a, int64_t *scratch) {
+    // `scratch`: kThreads / 32 + 4 int64 in shared memory.
+    __device__ __forceinline__ void start(const Args &a, int64_t *scratch) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         constexpr int kWarps = kThreads / 32;
         // the tiles of all sequences, kThreads of them at a time
@@ -163,9 +165,9 @@ struct Walk {
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) total += scratch[w];
         }
-        const Line line(total, gridDim.x);
+        line = Line(total, gridDim.x);
         at = end = 0;
-        if ((int)blockIdx.x >= line.parts) return line;
+        if ((int)blockIdx.x >= line.parts) return;
         at = line.begin(blockIdx.x);
         end = line.begin(blockIdx.x + 1);
         // the sequence that holds `at`: prefix sums
@@ -216,13 +218,19 @@ struct Walk {
             off -= n;
         }
         tile = (int)off;
-        return line;
     }
     __device__ __forceinline__ bool done() const { return at >= end; }
     __device__ __forceinline__ int segment() const { return max(1, span.n); }
     __device__ __forceinline__ int take() const {
         const int64_t n = segment() - tile, left = end - at;
         return (int)(n < left ? n : left);
+    }
+    // Of the segment here, which this part begins and does not finish.
+    __device__ __forceinline__ Cut cut_here() const {
+        Cut c;
+        c.cut = 1, c.n = line.part_of(at + segment() - 1) - (int)blockIdx.x + 1;
+        c.seq = b, c.head = head, c.block = block;
+        return c;
     }
     __device__ __forceinline__ void next(const Args &a) {
         at += take();
@@ -344,6 +352,26 @@ __device__ __forceinline__ void merge_cut(const Args &a) {
         for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], f);
     }
     store_row(a, s, c.head, row, lane, v);
+}
+
+constexpr int kJoinThreads = 128;
+template <int R>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
+    pdl_wait();
+    merge_cut<R, kJoinThreads>(a);
+}
+template <int R>
+void launch_join(const Args &a, int ctas, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, R / (kJoinThreads / 32));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, join_kernel<R>, a);
 }
 
 }  // namespace tq3_chunk
