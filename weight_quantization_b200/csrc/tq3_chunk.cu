@@ -290,12 +290,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
     if (tid == 0) cut->cut = 0;
     if (blockIdx.x == 0)
         for (int b = tid; b < a.batch; b += kThreads)
-            if (__ldg(a.kv_len + b) > (a.pages_per_seq << a.pools.shift)) atomicOr(&g_fault, tq3::kFaultPoolIndex);
+            if (__ldg(a.kv_len + b) > a.max_keys) atomicOr(&g_fault, tq3::kFaultPoolIndex);
 
+    float sg[4];
+    lane_signs(a, lane, sg);
     for (; !w.done(); w.next(a)) {
         const Seq s = w.seq;
         const int rows = s.new_tokens * a.group, r0 = w.block * R, before = s.keys - s.new_tokens;
-        const int p_lo = before + r0 / a.group, p_hi = before + (min(r0 + R, rows) - 1) / a.group;
+        const int p_lo = before + token_of(a, r0), p_hi = before + token_of(a, min(r0 + R, rows) - 1);
         const int take = w.take();
 
         steps.begin(w, p_hi);
@@ -309,7 +311,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
 #pragma unroll
             for (int n = 0; n < kEach; ++n) {
                 const int r = kWarps * n + warp;
-                load_row(a, s, w.head, r0 + r, lane, v[n]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[n][i] = 0.0f;
+                if (r0 + r < rows) load_row(a, s, w.head, r0 + r, lane, v[n]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[n][i] = __fmul_rn(v[n][i], sg[i]);
                 row_fwht(v[n], lane);
                 float m = fmaxf(fmaxf(fabsf(v[n][0]), fabsf(v[n][1])), fmaxf(fabsf(v[n][2]), fabsf(v[n][3])));
 #pragma unroll
@@ -358,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = r0 + 8 * n + 2 * t + e;
-                p[n][e] = r < rows ? before + r / a.group : -1;
+                p[n][e] = r < rows ? before + token_of(a, r) : -1;
             }
         }
         // the first and the second three bytes of a lane's 48 bits in the two words that hold them
@@ -559,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], f);
             if (whole) {
-                store_row(a, s, w.head, r0 + r, lane, v);
+                store_row(a, s, w.head, r0 + r, lane, sg, v);
             } else {
                 *reinterpret_cast<float4 *>(slot + r * 128 + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
                 if (lane == 0) slot[R * 128 + r] = sum == 0.0f ? -INFINITY : m, slot[R * 129 + r] = sum;
@@ -632,7 +638,10 @@ extern "C" wq_status tq3_attention_chunk(const void *q, int q_dtype, int64_t n_t
     a.pools = tq3_cache::Pools{const_cast<uint8_t *>(k_pool), const_cast<uint8_t *>(v_pool), n_pages, (int)kv_heads,
                                tq3_cache::page_shift(page_size)};
     a.table = page_table, a.q_start = q_start, a.kv_len = kv_len, a.pages_per_seq = pages_per_seq;
-    a.batch = (int)batch, a.n_tokens = (int)n_tokens, a.group = (int)group;
+    a.batch = (int)batch, a.n_tokens = (int)n_tokens;
+    tq3_chunk::set_group(a, (int)group);
+    const int64_t room = pages_per_seq > (tq3_chunk::kMaxKeys >> a.pools.shift) ? tq3_chunk::kMaxKeys : pages_per_seq << a.pools.shift;
+    a.max_keys = (int)room;
     a.window = (int)window, a.sinks = (int)sinks;
     a.rows_from = 0, a.rows_to = INT32_MAX;
     // post * softmax_scale * log2(e), rounded once

@@ -33,7 +33,10 @@ struct Args {
     tq3_cache::Pools pools;
     const int32_t *table, *q_start, *kv_len;
     int64_t pages_per_seq;
+    int max_keys;  // of a sequence: what its row of the table holds, kMaxKeys at most
     int batch, n_tokens, group;
+    uint32_t group_mul;  // r / group = (umulhi(group_mul, r) + r) >> group_shift for 0 <= r < 2^31
+    int group_shift;
     int window, sinks;  // window == 0: none
     int rows_from, rows_to;  // serves the sequences with rows_from <= rows per KV head < rows_to
     float coef;              // post * softmax_scale * log2(e)
@@ -43,22 +46,31 @@ struct Args {
     unsigned char *ws;
 };
 
+// Multiplier and shift of Args: with 2^(shift - 1) < group <= 2^shift, floor(2^32 (2^shift - group) / group) + 1
+// (division by an invariant, rounded up; r + umulhi stays below 2^32).
+inline void set_group(Args &a, int group) {
+    a.group = group;
+    a.group_shift = 0;
+    while ((int64_t(1) << a.group_shift) < group) ++a.group_shift;
+    a.group_mul = (uint32_t)((((uint64_t(1) << a.group_shift) - (uint64_t)group) << 32) / (uint64_t)group + 1);
+}
+// The token, from the first of the sequence's new ones, of row r.
+__device__ __forceinline__ int token_of(const Args &a, int r) {
+    return (int)((__umulhi(a.group_mul, (uint32_t)r) + (uint32_t)r) >> a.group_shift);
+}
+
 // A sequence's new tokens and keys, as this launch serves it.
 struct Seq {
     int start, new_tokens, keys;
 };
 
-__device__ __forceinline__ int clamp_int(int64_t v, int64_t lo, int64_t hi) {
-    return (int)(v < lo ? lo : v > hi ? hi : v);
-}
-
 __device__ __forceinline__ Seq load_seq(const Args &a, int b) {
     Seq s;
-    s.start = clamp_int(__ldg(a.q_start + b), 0, a.n_tokens);
-    s.new_tokens = clamp_int(__ldg(a.q_start + b + 1), s.start, a.n_tokens) - s.start;
-    const int64_t room = a.pages_per_seq << a.pools.shift;
-    s.keys = clamp_int(__ldg(a.kv_len + b), 0, room < kMaxKeys ? room : kMaxKeys);
-    const int64_t rows = (int64_t)s.new_tokens * a.group;
+    const int first = __ldg(a.q_start + b), next = __ldg(a.q_start + b + 1), keys = __ldg(a.kv_len + b);
+    s.start = min(max(first, 0), a.n_tokens);
+    s.new_tokens = min(max(next, s.start), a.n_tokens) - s.start;
+    s.keys = min(max(keys, 0), a.max_keys);
+    const int rows = s.new_tokens * a.group;
     if (rows < a.rows_from || rows >= a.rows_to) s.new_tokens = 0;
     return s;
 }
@@ -85,7 +97,7 @@ template <int R>
 __device__ __forceinline__ Span block_span(const Args &a, const Seq &s, int block) {
     const int r0 = block * R, r1 = min(r0 + R, s.new_tokens * a.group) - 1;
     const int before = s.keys - s.new_tokens;
-    return span_of(a, before + r0 / a.group, before + r1 / a.group);
+    return span_of(a, before + token_of(a, r0), before + token_of(a, r1));
 }
 
 // A block without a visible key still counts one tile: its rows are written as zeros.
@@ -96,6 +108,7 @@ __device__ __forceinline__ int blocks_of(const Args &a, const Seq &s) {
 template <int R>
 __device__ __forceinline__ int64_t tiles_of_head(const Args &a, const Seq &s) {
     int64_t n = 0;
+#pragma unroll 1
     for (int i = blocks_of<R>(a, s) - 1; i >= 0; --i) n += max(1, block_span<R>(a, s, i).n);
     return n;
 }
@@ -106,16 +119,15 @@ struct Line {
     int64_t each;
     int rest, parts;
     Line() = default;
+    // total < 2^47: two steps of a long division by a number below 2^15
     __device__ __forceinline__ Line(int64_t total, int ctas) {
         parts = total < ctas ? (int)total : ctas;
-        each = parts ? total / parts : 0;
-        rest = parts ? (int)(total - each * parts) : 0;
+        const uint32_t d = max(parts, 1), high = (uint32_t)(total >> 16), q = high / d;
+        const uint32_t low = (high - q * d) << 16 | (uint32_t)(total & 0xffff), r = low / d;
+        each = (int64_t)q << 16 | r;
+        rest = (int)(low - r * d);
     }
     __device__ __forceinline__ int64_t begin(int c) const { return each * c + min(c, rest); }
-    __device__ __forceinline__ int part_of(int64_t at) const {
-        const int64_t longer = (each + 1) * rest;
-        return (int)(at < longer ? at / (each + 1) : rest + (at - longer) / each);
-    }
 };
 
 // Header of a part, for the join: whether its last segment goes on in the next parts, how many parts it
@@ -154,6 +166,7 @@ struct Walk {
         constexpr int kWarps = kThreads / 32;
         // the tiles of all sequences, kThreads of them at a time
         int64_t total = 0;
+#pragma unroll 1
         for (int base = 0; base < a.batch; base += kThreads) {
             const int i = base + tid;
             int64_t c = i < a.batch ? tiles_of_head<R>(a, load_seq(a, i)) * a.pools.heads : 0;
@@ -165,13 +178,14 @@ struct Walk {
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) total += scratch[w];
         }
-        line = Line(total, gridDim.x);
+        line = Line(min(total, int64_t(1) << 46), gridDim.x);
         at = end = 0;
         if ((int)blockIdx.x >= line.parts) return;
         at = line.begin(blockIdx.x);
         end = line.begin(blockIdx.x + 1);
         // the sequence that holds `at`: prefix sums
         int64_t before = 0;
+#pragma unroll 1
         for (int base = 0;; base += kThreads) {
             const int i = base + tid;
             Seq s;
@@ -188,9 +202,13 @@ struct Walk {
             if (lane == 31) scratch[warp] = sum;
             __syncthreads();
             int64_t lead = before;
-            for (int w = 0; w < warp; ++w) lead += scratch[w];
             int64_t all = before;
-            for (int w = 0; w < kWarps; ++w) all += scratch[w];
+#pragma unroll 1
+            for (int w = 0; w < kWarps; ++w) {
+                const int64_t x = scratch[w];
+                all += x;
+                if (w < warp) lead += x;
+            }
             if (at >= lead + sum - c && at < lead + sum) {
                 scratch[kWarps] = i;
                 scratch[kWarps + 1] = at - (lead + sum - c);
@@ -208,9 +226,11 @@ struct Walk {
         seq.keys = (int)scratch[kWarps + 3];
         blocks = blocks_of<R>(a, seq);
         const int64_t per_head = tiles_of_head<R>(a, seq);
-        head = (int)(off / per_head);
-        off -= head * per_head;
+        head = 0;
+#pragma unroll 1
+        for (; off >= per_head; off -= per_head) ++head;
         block = 0;
+#pragma unroll 1
         for (;; ++block) {
             span = block_span<R>(a, seq, block);
             const int n = max(1, span.n);
@@ -228,7 +248,10 @@ struct Walk {
     // Of the segment here, which this part begins and does not finish.
     __device__ __forceinline__ Cut cut_here() const {
         Cut c;
-        c.cut = 1, c.n = line.part_of(at + segment() - 1) - (int)blockIdx.x + 1;
+        c.cut = 1, c.n = 2;
+        const int64_t last = at + segment();
+#pragma unroll 1
+        for (int part = blockIdx.x + 2; part < line.parts && line.begin(part) < last; ++part) ++c.n;
         c.seq = b, c.head = head, c.block = block;
         return c;
     }
@@ -274,32 +297,33 @@ __device__ __forceinline__ float sign_of(const SignMask &m, int e) {
     return __uint_as_float(0x3f800000u | (~(m.w[e >> 5] >> (e & 31)) & 1u) << 31);
 }
 
-// Elements 4 l .. 4 l + 3 of row `row` of (sequence, head), with the sign flips; zeros past the rows.
+// A lane's four elements of a row: their sign flips.
+__device__ __forceinline__ void lane_signs(const Args &a, int lane, float (&sg)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sg[i] = sign_of(a.mask, 4 * lane + i);
+}
+// Elements 4 l .. 4 l + 3 of row `row` of (sequence, head).
 __device__ __forceinline__ void load_row(const Args &a, const Seq &s, int head, int row, int lane, float (&v)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = 0.0f;
-    if (row < s.new_tokens * a.group) {
-        const int64_t at = (int64_t)(s.start + row / a.group) * a.q_token +
-                           (int64_t)(head * a.group + row % a.group) * a.q_head + 4 * lane;
-        if (a.q_bf16) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + at));
-            v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
-        } else {
-            const float4 w = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at));
-            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-        }
+    const int token = token_of(a, row);
+    const int64_t at = (int64_t)(s.start + token) * a.q_token + (int64_t)(head * a.group + row - token * a.group) * a.q_head +
+                       4 * lane;
+    if (a.q_bf16) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + at));
+        v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+    } else {
+        const float4 w = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at));
+        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], sign_of(a.mask, 4 * lane + i));
 }
 
 // out = s . H(row) post, from the rotated basis.
-__device__ __forceinline__ void store_row(const Args &a, const Seq &s, int head, int row, int lane, float (&v)[4]) {
+__device__ __forceinline__ void store_row(const Args &a, const Seq &s, int head, int row, int lane, const float (&sg)[4],
+                                          float (&v)[4]) {
     row_fwht(v, lane);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], tq3::fwht_post()), sign_of(a.mask, 4 * lane + i));
-    const int64_t at = ((int64_t)(s.start + row / a.group) * a.pools.heads * a.group + head * a.group + row % a.group) * 128 +
-                       4 * lane;
+    for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], tq3::fwht_post()), sg[i]);
+    const int token = token_of(a, row);
+    const int64_t at = (((int64_t)(s.start + token) * a.pools.heads + head) * a.group + row - token * a.group) * 128 + 4 * lane;
     if (a.out_bf16)
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
@@ -351,7 +375,9 @@ __device__ __forceinline__ void merge_cut(const Args &a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], f);
     }
-    store_row(a, s, c.head, row, lane, v);
+    float sg[4];
+    lane_signs(a, lane, sg);
+    store_row(a, s, c.head, row, lane, sg, v);
 }
 
 constexpr int kJoinThreads = 128;

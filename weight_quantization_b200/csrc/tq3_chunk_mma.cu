@@ -3,8 +3,8 @@
 // segment has NB x 128 rows and a tile of 128 keys is two products per 128 rows:
 //     S = Q~ K^T       (128 rows x 128 keys, K = 128 rotated coordinates; both operands in shared memory)
 //     O += P V         (128 rows x 128 coordinates, K = 128 keys; P in tensor memory, V in shared memory)
-// with K's row j = c[idx_j] f_j coef 2^-u and V's row j = c[idx'_j] g_j 2^13 / G in fp16. 2^u brings the
-// largest sum of |q| of the segment's rows, a bound of |q~|, to 2^4 .. 2^5, so that S is the logit in log2 units as it leaves the tensor
+// with K's row j = c[idx_j] f_j coef 2^-u and V's row j = c[idx'_j] g_j 2^13 / G in fp16. 2^u brings a
+// bound of the segment's |q~| to 2^7 .. 2^8, so that S is the logit in log2 units as it leaves the tensor
 // core and the softmax has no per-key factor to apply. What underflows in K then moves a logit by less
 // than 2^-13, and only the absolute error of a logit matters. G follows the largest g_j of the tiles so
 // far and is raised when one is passed by 4 (O is rescaled then), so a value keeps all its bits down to
@@ -54,7 +54,8 @@ constexpr int kBox = 128 * 128;       // 64 coordinates of a 128-row fp16 operan
 constexpr int kOp = 2 * kBox;
 constexpr uint32_t kMaxPolls = 1u << 24;
 constexpr float kLazy = 8.0f, kLift = 6.0f;  // as in tq3_chunk.cu
-constexpr int kQBits = 4;             // |q~| of a segment is scaled to less than 2^5
+constexpr int kRecStages = 2, kRecBytes = 2 * kTileKeys * tq3_cache::kRec;
+constexpr int kQBits = 7;             // a bound of |q~| of a segment is scaled to 2^7 .. 2^8
 constexpr float kVTop = 8192.0f;      // a value of factor G has this one
 
 // fp16 operands, fp32 accumulator, M = N = 128; B of the value product is MN-major.
@@ -72,8 +73,10 @@ struct Cfg {
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + NB * kParts * kOp;
     static constexpr int kOffV = kOffK + KS * kParts * kOp;
-    static constexpr int kOffShared = kOffV + KS * kParts * kOp;
+    static constexpr int kOffRec = kOffV + KS * kParts * kOp;  // a tile's key records, then its value records
+    static constexpr int kOffShared = kOffRec + kRecStages * kRecBytes;
     static constexpr int kSmem = 1024 + kOffShared + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     // centroids times kGain: see tq3_chunk.cu
     static constexpr float kGain = kWide ? 1.0f : 1.6196665f;
     // tensor memory: S, O, and P (over S where two blocks fill the memory)
@@ -120,33 +123,56 @@ __device__ __forceinline__ uint32_t fma_h2(uint32_t a, uint32_t b, uint32_t c) {
     return r;
 }
 
-// 16-byte chunk `chunk` (elements 8 chunk on) of row `row` of an operand: two boxes of 64 elements, rows
-// of 128 bytes, 128-byte swizzle.
-__device__ __forceinline__ uint4 *op_chunk(unsigned char *op, int row, int chunk) {
-    return reinterpret_cast<uint4 *>(op + (chunk >> 3) * kBox + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
-}
-// The same tile as an MN-major operand (rows are K, their elements N): atoms of 64 elements x 8 rows, the
-// next 64 elements a box further (leading offset), the next 8 rows 1024 bytes further (stride offset).
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kBox >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-// D[tmem] (+)= A[tmem] * B.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Operand descriptors as their low words (address, leading offset); the high word is the same for both:
+// the next 8 rows 1024 bytes further, version 1, 128-byte swizzle. K-major ignores the leading offset; for
+// the same tile as an MN-major operand (its rows are K) it is the step to the next 64 elements, a box.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t k_desc(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t mn_desc(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4 | (uint32_t)(kBox >> 4) << 16; }
+// D[tmem] (+)= A B^T, A and B in shared memory; and with A in tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
+        : "memory");
+}
+// Writes 16 consecutive tensor-memory columns of this thread's lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
+// Waits for a phase for kWaitLimitNs at most. The clock is first read after some microseconds of polls:
+// reading it costs more than most of these waits last.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t phase) {
-    uint32_t ok;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(phase)
-                 : "memory");
-    return ok || mbar_wait_bounded(bar, phase, kMaxPolls);
+    const uint32_t at = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t it = 0; it < kMaxPolls; ++it) {
+        uint32_t ok;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok)
+                     : "r"(at), "r"(phase)
+                     : "memory");
+        if (ok) return true;
+        if ((it & 255) == 255) {
+            if (t0 == 0)
+                t0 = global_ns();
+            else if (global_ns() - t0 > kWaitLimitNs)
+                return false;
+        }
+    }
+    return false;
 }
 // The whole warp waits; false sets the fault bit.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase) {
@@ -158,38 +184,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase) {
 template <int kBar, int kCount>
 __device__ __forceinline__ void named_sync() {
     asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kCount) : "memory");
-}
-
-// Unnormalised 64-point FWHT of a thread's values. Half `h` of a 128-point one is that of the sums
-// (h = 0) or the differences (h = 1) of the two halves of its input, so a thread never holds 128 values.
-__device__ __forceinline__ void fwht64(float (&v)[64]) {
-#pragma unroll
-    for (int i = 0; i < 64; i += 2) {
-        const float a = v[i], b = v[i + 1];
-        v[i] = __fadd_rn(a, b);
-        v[i + 1] = __fsub_rn(a, b);
-    }
-#pragma unroll
-    for (int h = 2; h < 64; h <<= 1)
-#pragma unroll
-        for (int i = 0; i < 64; i += 2)
-            if ((i & h) == 0) {
-                const f32x2 a = pk2(v[i], v[i + 1]), b = pk2(v[i + h], v[i + h + 1]);
-                upk2(add2(a, b), v[i], v[i + 1]);
-                upk2(sub2(a, b), v[i + h], v[i + h + 1]);
-            }
-}
-// Elements e .. e + 7 of a query row.
-__device__ __forceinline__ void load8(const Args &a, int64_t at, int e, float (&x)[8]) {
-    if (a.q_bf16) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at + e));
-        x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
-        x[4] = bf16_lo(w.z), x[5] = bf16_hi(w.z), x[6] = bf16_lo(w.w), x[7] = bf16_hi(w.w);
-    } else {
-        const float4 *const p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at + e);
-        const float4 u = __ldg(p), v = __ldg(p + 1);
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-    }
 }
 
 // Four fp16 centroids a selector: the low and the high bytes of the eight values, in two words each.
@@ -219,38 +213,43 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t x) {
     return y + (y & 0x38383838u);
 }
 
-// The 128 centroids of a record's indices times a factor, into row `row` of an operand. hi + lo is the
-// factor, as pairs of equal halves.
+// The 128 centroids of a record's indices times a factor, into row `row` of an operand, 32 at a time (the
+// loop is kept small: the roles' loops share the instruction cache). hi + lo is the factor.
 template <bool kWide>
-__device__ __forceinline__ void expand(unsigned char *op, int row, const uint32_t (&w)[12], const Table &th, const Table &tl,
+__device__ __forceinline__ void expand(unsigned char *op, int row, const uint32_t *rec, const Table &th, const Table &tl,
                                        float factor) {
     const uint32_t fh = h2(factor, factor);
     const float rest = __fsub_rn(factor, f2(fh).x);
     const uint32_t fl = h2(rest, rest);
+#pragma unroll 1
+    for (int part = 0; part < 4; ++part) {
+        const uint32_t w0 = rec[3 * part], w1 = rec[3 * part + 1], w2 = rec[3 * part + 2];
+        unsigned char *const to = op + (part >> 1) * kBox + row * 128;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        const int o = 24 * c, q = o >> 5, s = o & 31;
-        const uint32_t sel = nibbles(s == 0 ? w[q] : s == 8 ? w[q] >> 8 : __funnelshift_r(w[q], w[q + 1 < 12 ? q + 1 : q], s));
-        uint32_t ch[4];
-        four(th, sel, ch[0], ch[1]);
-        four(th, sel >> 16, ch[2], ch[3]);
-        uint32_t h[4];
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t x = c == 0 ? w0 : c == 1 ? __funnelshift_r(w0, w1, 24) : c == 2 ? __funnelshift_r(w1, w2, 16) : w2 >> 8;
+            const uint32_t sel = nibbles(x);
+            uint32_t ch[4], h[4];
+            four(th, sel, ch[0], ch[1]);
+            four(th, sel >> 16, ch[2], ch[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = mul_h2(ch[i], fh);
-        if (kWide) {
-            // hi = RN(ch fh); lo = (ch fh - hi) + ch fl + cl fh, the difference exact
-            uint32_t cl[4], l[4];
-            four(tl, sel, cl[0], cl[1]);
-            four(tl, sel >> 16, cl[2], cl[3]);
+            for (int i = 0; i < 4; ++i) h[i] = mul_h2(ch[i], fh);
+            uint4 *const chunk = reinterpret_cast<uint4 *>(to + (((4 * (part & 1) + c) ^ (row & 7)) << 4));
+            if (kWide) {
+                // hi = RN(ch fh); lo = (ch fh - hi) + ch fl + cl fh, the difference exact
+                uint32_t cl[4], l[4];
+                four(tl, sel, cl[0], cl[1]);
+                four(tl, sel >> 16, cl[2], cl[3]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                l[i] = fma_h2(cl[i], fh, fma_h2(ch[i], fl, fma_h2(ch[i], fh, h[i] ^ 0x80008000u)));
-            *op_chunk(op + kOp, row, c) = make_uint4(l[0], l[1], l[2], l[3]);
-        } else {
+                for (int i = 0; i < 4; ++i)
+                    l[i] = fma_h2(cl[i], fh, fma_h2(ch[i], fl, fma_h2(ch[i], fh, h[i] ^ 0x80008000u)));
+                *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(chunk) + kOp) = make_uint4(l[0], l[1], l[2], l[3]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = fma_h2(ch[i], fl, h[i]);
+                for (int i = 0; i < 4; ++i) h[i] = fma_h2(ch[i], fl, h[i]);
+            }
+            *chunk = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        *op_chunk(op, row, c) = make_uint4(h[0], h[1], h[2], h[3]);
     }
 }
 
@@ -276,7 +275,7 @@ struct Segment {
         s = w.seq, span = w.span, b = w.b, head = w.head;
         rows = s.new_tokens * a.group, r0 = w.block * R, before = s.keys - s.new_tokens;
         take = w.take(), first = w.tile;
-        p_hi = before + (min(r0 + R, rows) - 1) / a.group;
+        p_hi = before + token_of(a, min(r0 + R, rows) - 1);
         nb = Cfg<kWide>::NB == 2 && r0 + kBlock < rows ? 2 : 1;
         blind = p_hi < 0;
         whole = first == 0 && take == w.segment();
@@ -303,66 +302,57 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
     using C = Cfg<kWide>;
     constexpr int NB = C::NB, KS = C::KS, R = C::R;
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, blk = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + blk * 128 + lanes, tO = tmem + C::kTmemO + blk * 128 + lanes,
+                   tP = tmem + C::kTmemP + blk * 128 + lanes;
     bool dead = false;
     uint32_t n_tile = 0, n_s = 0, n_out = 0;  // tiles; of this warp's block: S products, results
+    float sg[4];
+    lane_signs(a, lane, sg);
     while (!w.done()) {
         const Segment<kWide> g(a, w);
-        const int blk = warp >> 2;
-        const int rr = blk * kBlock + (warp & 3) * 32 + lane, row = g.r0 + rr;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int wr = g.r0 + 32 * warp, n_rows = min(32, g.rows - wr);  // the warp's rows; may be none
         {
-            // |q~| is at most the row's sum of |q|, which decides the scale
-            const int64_t at = row < g.rows ? (int64_t)(g.s.start + row / a.group) * a.q_token +
-                                                (int64_t)(g.head * a.group + row % a.group) * a.q_head
-                                          : -1;
+            // |q~| is at most the sum of |q| over a row, that is 32 times the largest sum over a lane
             float m = 0.0f;
-            if (at >= 0)
 #pragma unroll 4
-                for (int c = 0; c < 16; ++c) {
-                    float x[8];
-                    load8(a, at, 8 * c, x);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) m = __fadd_rn(m, fabsf(x[i]));
-                }
-            if (!(m < INFINITY)) m = 0.0f;  // a row that is not finite spoils only itself
+            for (int r = 0; r < n_rows; ++r) {
+                float v[4];
+                load_row(a, g.s, g.head, wr + r, lane, v);
+                const float x = __fadd_rn(__fadd_rn(fabsf(v[0]), fabsf(v[1])), __fadd_rn(fabsf(v[2]), fabsf(v[3])));
+                m = x < INFINITY ? fmaxf(m, x) : m;  // a row that is not finite spoils only itself
+            }
 #pragma unroll
             for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (lane == 0) sh.top[warp] = m;
             named_sync<1, 128 * NB>();
 #pragma unroll
             for (int i = 0; i < 4 * NB; ++i) m = fmaxf(m, sh.top[i]);
-            // 2^u and 2^-u with u = kQBits - exponent, by biased exponents
-            const int e = max(kQBits + 1, min(253, (int)(__float_as_uint(m) >> 23)));
+            m = fminf(m, 0x1p120f);
+            // 2^u and 2^-u with u = kQBits - exponent of 32 m, by biased exponents
+            const int e = max(kQBits + 1, (int)(__float_as_uint(__fmul_rn(m, 32.0f)) >> 23));
             const int up_exp = min(254, 254 + kQBits - e);
             const float up = __uint_as_float((uint32_t)up_exp << 23);
             if (tid == 0) sh.down = __uint_as_float((uint32_t)(254 - up_exp) << 23);
-            unsigned char *const op = base + C::kOffQ + blk * C::kParts * kOp;
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                float v[64];
-                const float sgn = half ? -1.0f : 1.0f;
+            unsigned char *const op = base + C::kOffQ + blk * C::kParts * kOp + (lane >> 4) * kBox + 8 * (lane & 1);
+#pragma unroll 2
+            for (int r = 0; r < 32; ++r) {
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (r < n_rows) load_row(a, g.s, g.head, wr + r, lane, v);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    float x[8] = {}, y[8] = {};
-                    if (at >= 0) load8(a, at, 8 * c, x), load8(a, at, 64 + 8 * c, y);
+                for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], sg[i]);
+                row_fwht(v, lane);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        v[8 * c + i] = __fmaf_rn(__fmul_rn(y[i], sign_of(a.mask, 64 + 8 * c + i)), sgn,
-                                                 __fmul_rn(x[i], sign_of(a.mask, 8 * c + i)));
-                }
-                fwht64(v);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t h[4], l[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float x = __fmul_rn(v[8 * c + 2 * i], up), y = __fmul_rn(v[8 * c + 2 * i + 1], up);
-                        h[i] = h2(x, y);
-                        if (kWide) l[i] = h2(__fsub_rn(x, f2(h[i]).x), __fsub_rn(y, f2(h[i]).y));
-                    }
-                    *op_chunk(op, rr & 127, 8 * half + c) = make_uint4(h[0], h[1], h[2], h[3]);
-                    if (kWide) *op_chunk(op + kOp, rr & 127, 8 * half + c) = make_uint4(l[0], l[1], l[2], l[3]);
+                for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], up);
+                const int row = (warp & 3) * 32 + r;
+                unsigned char *const to = op + row * 128 + (((lane >> 1 & 7) ^ (row & 7)) << 4);
+                const uint2 hi = make_uint2(h2(v[0], v[1]), h2(v[2], v[3]));
+                *reinterpret_cast<uint2 *>(to) = hi;
+                if (kWide) {
+                    const float2 x = f2(hi.x), y = f2(hi.y);
+                    *reinterpret_cast<uint2 *>(to + kOp) =
+                        make_uint2(h2(__fsub_rn(v[0], x.x), __fsub_rn(v[1], x.y)), h2(__fsub_rn(v[2], y.x), __fsub_rn(v[3], y.y)));
                 }
             }
             fence_proxy_async_smem();
@@ -370,13 +360,11 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
             if (lane == 0) mbar_arrive(&sh.q_ready);
         }
         float M = -FLT_MAX, sum = 0.0f, G = 1.0f;
-        const uint32_t tS = tmem + blk * 128 + lanes, tO = tmem + C::kTmemO + blk * 128 + lanes,
-                       tP = tmem + C::kTmemP + blk * 128 + lanes;
         if (blk < g.nb && !g.blind && !dead) {
-            const int pos = row < g.rows ? g.before + row / a.group : -1;
+            const int pos = lane < n_rows ? g.before + token_of(a, wr + lane) : -1;
             // positions of the warp's rows, for tiles that all of them see whole
-            const int wr = g.r0 + blk * kBlock + (warp & 3) * 32;
-            const int lo = g.before + min(wr, g.rows - 1) / a.group, hi = g.before + min(wr + 31, g.rows - 1) / a.group;
+            const int lo = g.before + token_of(a, min(wr, g.rows - 1)), hi = g.before + token_of(a, min(wr + 31, g.rows - 1));
+#pragma unroll 1
             for (int i = 0; i < g.take; ++i) {
                 const uint32_t n = n_tile + i, st = n % KS;
                 const int j0 = g.span.tile(g.first + i) * kTileKeys;
@@ -390,57 +378,70 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
                 const bool full = (t.valid[0] & t.valid[1] & t.valid[2] & t.valid[3]) == 0xffffffffu &&
                                   j0 + kTileKeys <= lo + 1 &&
                                   (a.window == 0 || j0 > hi - a.window || j0 + kTileKeys <= a.sinks);
-                float scale = t.ratio;  // of O, before this tile's product
-                G = t.G;
-                uint32_t P[kWide ? 1 : 64];
-                float psum;
-                for (int pass = 0; pass < 2; ++pass) {
-                    const float Mo = __fsub_rn(M, kLift);
-                    const f32x2 M2 = pk2(Mo, Mo);
-                    float mx = -INFINITY;
-                    f32x2 ps = pk2(0.0f, 0.0f);
-#pragma unroll
+                if (!full) {  // -inf where the row does not see the key
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         float x[32];
                         tmem_ld32(tS + 32 * c, x);
                         tmem_wait(x);
-                        if (!full) {
-                            const uint32_t on = visible(a, pos, j0 + 32 * c) & t.valid[c];
+                        const uint32_t on = visible(a, pos, j0 + 32 * c) & t.valid[c];
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(on >> k & 1u)) x[k] = -INFINITY;
-                        }
-                        uint32_t pk[32];
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            mx = max3(mx, x[k], x[k + 1]);
-                            float d0, d1;
-                            upk2(sub2(pk2(x[k], x[k + 1]), M2), d0, d1);
-                            d0 = ex2(d0), d1 = ex2(d1);
-                            ps = add2(ps, pk2(d0, d1));
-                            const uint32_t h = h2(d0, d1);
-                            if (kWide) {
-                                pk[k / 2] = h;
-                                pk[16 + k / 2] = h2(__fsub_rn(d0, f2(h).x), __fsub_rn(d1, f2(h).y));
-                            } else {
-                                P[kWide ? 0 : 16 * c + k / 2] = h;
-                            }
-                        }
-                        if (kWide) tmem_st32(tP + 32 * c, *reinterpret_cast<const float(*)[32]>(pk));
+                        for (int k = 0; k < 32; ++k) x[k] = (on >> k & 1u) ? x[k] : -INFINITY;
+                        tmem_st32(tS + 32 * c, x);
                     }
-                    float s0, s1;
-                    upk2(ps, s0, s1);
-                    psum = __fadd_rn(s0, s1);
-                    const bool raise = mx > __fadd_rn(M, kLazy);
-                    if (!__any_sync(0xffffffffu, raise)) break;
-                    // every row of the warp takes its own maximum
+                    tmem_st_wait();
+                }
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    float x[32], y[32];
+                    tmem_ld32(tS + 64 * c, x);
+                    tmem_ld32(tS + 64 * c + 32, y);
+                    tmem_wait(x);
+                    tmem_wait(y);
+                    float m0 = x[0], m1 = y[0];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) m0 = max3(m0, x[k], x[k + 1]), m1 = max3(m1, y[k], y[k + 1]);
+                    mx = max3(mx, m0, m1);
+                }
+                float scale = t.ratio;  // of O, before this tile's product
+                G = t.G;
+                if (__any_sync(0xffffffffu, mx > __fadd_rn(M, kLazy))) {  // every row of the warp takes its own maximum
                     const float m = fmaxf(M, mx), alpha = ex2(__fsub_rn(M, m));
                     M = m;
                     sum = __fmul_rn(sum, alpha);
                     scale = __fmul_rn(scale, alpha);
                 }
-                if (i > 0 && __any_sync(0xffffffffu, scale != 1.0f)) {
+                const float Mo = __fsub_rn(M, kLift);
+                const f32x2 M2 = pk2(Mo, Mo);
+                f32x2 ps0 = pk2(0.0f, 0.0f), ps1 = ps0;
+                // P's 16 columns of a step lie over columns of S that have been read
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    float x[32];
+                    tmem_ld32(tS + 32 * c, x);
+                    tmem_wait(x);
+                    uint32_t p[16], l[16];
 #pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float d0, d1;
+                        upk2(sub2(pk2(x[2 * k], x[2 * k + 1]), M2), d0, d1);
+                        d0 = ex2(d0), d1 = ex2(d1);
+                        if (k & 1)
+                            ps1 = add2(ps1, pk2(d0, d1));
+                        else
+                            ps0 = add2(ps0, pk2(d0, d1));
+                        p[k] = h2(d0, d1);
+                        if (kWide) l[k] = h2(__fsub_rn(d0, f2(p[k]).x), __fsub_rn(d1, f2(p[k]).y));
+                    }
+                    tmem_st16(tP + (kWide ? 32 : 16) * c, p);
+                    if (kWide) tmem_st16(tP + 32 * c + 16, l);
+                }
+                float s0, s1;
+                upk2(add2(ps0, ps1), s0, s1);
+                sum = __fadd_rn(sum, __fadd_rn(s0, s1));
+                if (i > 0 && __any_sync(0xffffffffu, scale != 1.0f)) {
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         float o[32];
                         tmem_ld32(tO + 32 * c, o);
@@ -449,11 +450,6 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
                         for (int k = 0; k < 32; ++k) o[k] = __fmul_rn(o[k], scale);
                         tmem_st32(tO + 32 * c, o);
                     }
-                }
-                sum = __fadd_rn(sum, psum);
-                if (!kWide) {
-                    tmem_st32(tP, *reinterpret_cast<const float(*)[32]>(&P[0]));
-                    tmem_st32(tP + 32, *reinterpret_cast<const float(*)[32]>(&P[kWide ? 0 : 32]));
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -464,57 +460,41 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
             ++n_out;
             tc_fence_after();
         }
-        // this thread's row: finished, or a part of a cut segment
-        if (blk < g.nb && !dead) {
+        // the rows: finished, or a part of a cut segment. Their sums pass through shared memory (Q and K:
+        // every S product is done) from a thread a row to a warp a row
+        if (n_rows > 0 && !dead) {
             const float f = g.blind || sum == 0.0f ? 0.0f : __fmul_rn(__frcp_rn(sum), __fmul_rn(G, 1.0f / (kVTop * C::kGain)));
+            unsigned char *const stage = base + C::kOffQ + warp * 16384;
+            if (!g.blind) {
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                const float sgn = half ? -1.0f : 1.0f;
-                float v[64];
+                for (int c = 0; c < 4; ++c) {
+                    float x[32];
+                    tmem_ld32(tO + 32 * c, x);
+                    tmem_wait(x);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x[32], y[32];
-                    if (!g.blind) {
-                        tmem_ld32(tO + 32 * c, x);
-                        tmem_ld32(tO + 64 + 32 * c, y);
-                        tmem_wait(x);
-                        tmem_wait(y);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (f == 0.0f) x[i] = y[i] = 0.0f;
-                        v[32 * c + i] = g.whole ? __fmul_rn(__fmaf_rn(y[i], sgn, x[i]), f) : __fmul_rn(half ? y[i] : x[i], f);
-                    }
-                }
-                if (row < g.rows && g.whole) {
-                    fwht64(v);
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        const float flip = half ? sign_of(a.mask, 64 + i) : sign_of(a.mask, i);
-                        v[i] = __fmul_rn(__fmul_rn(v[i], tq3::fwht_post()), flip);
-                    }
-                    const int64_t at = ((int64_t)(g.s.start + row / a.group) * a.pools.heads * a.group + g.head * a.group +
-                                        row % a.group) * 128 + 64 * half;
-                    if (a.out_bf16) {
-                        uint4 *const to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            to[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                               pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-                    } else {
-                        float4 *const to = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) to[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    }
-                } else if (row < g.rows) {
-                    float *const slot = slot_at<R>(a, gridDim.x, 2 * blockIdx.x + (g.first == 0));
-                    float4 *const to = reinterpret_cast<float4 *>(slot + rr * 128 + 64 * half);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) to[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    slot[R * 128 + rr] = sum == 0.0f ? -INFINITY : M;
-                    slot[R * 129 + rr] = sum;
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<float4 *>(stage + 512 * lane + (((8 * c + k) ^ lane) << 4)) =
+                            make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
                 }
                 __syncwarp();
+            }
+            float *const slot = slot_at<R>(a, gridDim.x, 2 * blockIdx.x + (g.first == 0));
+#pragma unroll 2
+            for (int r = 0; r < n_rows; ++r) {
+                const float fr = __shfl_sync(0xffffffffu, f, r);
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (fr != 0.0f) {
+                    const float4 x = *reinterpret_cast<const float4 *>(stage + 512 * r + ((lane ^ r) << 4));
+                    v[0] = __fmul_rn(x.x, fr), v[1] = __fmul_rn(x.y, fr), v[2] = __fmul_rn(x.z, fr), v[3] = __fmul_rn(x.w, fr);
+                }
+                if (g.whole)
+                    store_row(a, g.s, g.head, wr + r, lane, sg, v);
+                else
+                    *reinterpret_cast<float4 *>(slot + (32 * warp + r) * 128 + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+            if (!g.whole && lane < n_rows) {
+                slot[R * 128 + 32 * warp + lane] = sum == 0.0f ? -INFINITY : M;
+                slot[R * 129 + 32 * warp + lane] = sum;
             }
         }
         n_tile += g.blind ? 0 : g.take;
@@ -523,13 +503,17 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
     return dead;
 }
 
-// Warps 8 .. 11.
+__device__ __forceinline__ void cp_async8(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Warps 8 .. 11: a thread a key, of both pools.
 template <bool kWide>
 __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned char *base) {
     using C = Cfg<kWide>;
     constexpr int KS = C::KS, R = C::R;
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, key = tid - 256;
     bool dead = false;
     uint32_t n_tile = 0, segs = 0;
     Table th, tl;
@@ -547,56 +531,62 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
     }
     while (!w.done()) {
         const Segment<kWide> g(a, w);
-        const int key = tid - 256;
-        uint2 rk[7], rv[7];
-        bool ok = false, ok_next = false;
-        // this thread's key of tile i: whether a row needs it, and its records
-        auto load = [&](int i) {
-            ok_next = false;
-            if (i < g.take) {
+        const int take = g.blind ? 0 : g.take;
+        // Two steps ahead of a tile its page entry is asked for, one step ahead its records. -1: no row
+        // needs this thread's key (of no tile, or behind a window); -2: an entry outside the pool.
+        int32_t entry = -1;
+        uint32_t have = 0;  // bit i % kRecStages: the key of tile i has a page
+        auto ask = [&](int i) {
+            entry = -1;
+            if (i < take) {
                 const int j = g.span.tile(g.first + i) * kTileKeys + key;
                 if (j <= g.p_hi && (j >= g.span.from || j < g.span.until)) {
-                    const int32_t page = __ldg(a.table + g.b * a.pages_per_seq + (j >> a.pools.shift));
-                    if (page >= 0 && page < a.pools.n_pages) {
-                        const int64_t at = tq3_cache::record_at(a.pools, page, g.head, j & ((1 << a.pools.shift) - 1));
-#pragma unroll
-                        for (int x = 0; x < 7; ++x) {
-                            rk[x] = __ldg(reinterpret_cast<const uint2 *>(a.pools.k + at) + x);
-                            rv[x] = __ldg(reinterpret_cast<const uint2 *>(a.pools.v + at) + x);
-                        }
-                        ok_next = true;
-                    } else {
-                        atomicOr(&g_fault, tq3::kFaultPoolIndex);
-                    }
+                    entry = __ldg(a.table + g.b * a.pages_per_seq + (j >> a.pools.shift));
+                    if (entry < 0) entry = -2;
                 }
             }
         };
-        float G = 0.0f;
-        if (!g.blind) {
-            load(0);
-            if (!dead && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
-        }
-        const float coef = __fmul_rn(__fmul_rn(a.coef, 1.0f / C::kGain), sh.down);
-        for (int i = 0; i < g.take && !g.blind; ++i) {
-            const uint32_t n = n_tile + i, st = n % KS, use = n / KS;
-            ok = ok_next;
-            uint32_t wk[12], wv[12];
-            float fk = 0.0f, gv = 0.0f;
-            if (ok) {
+        auto fetch = [&](int i) {  // the records of tile i, whose entry is in hand
+            const uint32_t bit = 1u << (i % kRecStages);
+            have &= ~bit;
+            if (i < take) {
+                const int j = g.span.tile(g.first + i) * kTileKeys + key;
+                const bool ok = entry >= 0 && entry < a.pools.n_pages;
+                if (entry != -1 && !ok) atomicOr(&g_fault, tq3::kFaultPoolIndex);
+                if (ok) have |= bit;
+                const int64_t at = ok ? tq3_cache::record_at(a.pools, entry, g.head, j & ((1 << a.pools.shift) - 1)) : 0;
+                const uint32_t to = smem_u32(base + C::kOffRec + (i % kRecStages) * kRecBytes) + key * tq3_cache::kRec;
+                const uint32_t bytes = ok ? 8 : 0;  // nothing is read for 0 bytes, zeros are written
 #pragma unroll
-                for (int x = 0; x < 6; ++x) wk[2 * x] = rk[x].x, wk[2 * x + 1] = rk[x].y, wv[2 * x] = rv[x].x, wv[2 * x + 1] = rv[x].y;
-                fk = __fmul_rn(__fmul_rn(__uint_as_float(rk[6].x), __uint_as_float(rk[6].y)), coef);
-                gv = __fmul_rn(__uint_as_float(rv[6].x), __uint_as_float(rv[6].y));
-                if (!(fabsf(gv) < INFINITY)) fk = __uint_as_float(0x7fffffffu), gv = 0.0f;
-            } else {
-#pragma unroll
-                for (int x = 0; x < 12; ++x) wk[x] = wv[x] = 0u;
+                for (int x = 0; x < 7; ++x) {
+                    cp_async8(to + 8 * x, a.pools.k + at + 8 * x, bytes);
+                    cp_async8(to + kRecBytes / 2 + 8 * x, a.pools.v + at + 8 * x, bytes);
+                }
             }
-            load(i + 1);
-            // the largest factor of the tile
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        float G = 0.0f;
+        ask(0);
+        fetch(0);
+        ask(1);
+        if (take > 0 && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
+        const float coef = __fmul_rn(__fmul_rn(a.coef, 1.0f / C::kGain), sh.down);
+#pragma unroll 1
+        for (int i = 0; i < take; ++i) {
+            const uint32_t n = n_tile + i, st = n % KS, use = n / KS;
+            fetch(i + 1);
+            ask(i + 2);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");  // a thread reads only what it copied
+            const uint32_t *const rec =
+                reinterpret_cast<const uint32_t *>(base + C::kOffRec + (i % kRecStages) * kRecBytes + key * tq3_cache::kRec);
+            const float2 rk = *reinterpret_cast<const float2 *>(rec + 12),
+                         rv = *reinterpret_cast<const float2 *>(rec + kRecBytes / 8 + 12);
+            float fk = __fmul_rn(__fmul_rn(rk.x, rk.y), coef), gv = __fmul_rn(rv.x, rv.y);
+            if (!(fabsf(gv) < INFINITY)) fk = __uint_as_float(0x7fffffffu), gv = 0.0f;
+            // the largest factor of the tile (the four warps leave together: a warp whose wait ran out
+            // says so here)
             const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(gv)));
-            const uint32_t valid = __ballot_sync(0xffffffffu, ok);
-            // (the four warps leave together: a warp whose wait ran out says so here)
+            const uint32_t valid = __ballot_sync(0xffffffffu, (have >> (i % kRecStages)) & 1u);
             if (lane == 0) sh.gmax[n & 1][warp - 8] = dead ? 0xffffffffu : top;
             named_sync<2, 128>();
             uint32_t all = 0;
@@ -609,36 +599,35 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
             const float most = __uint_as_float(all);
             float ratio = 1.0f;
             if (G == 0.0f || most > 4.0f * G) {
-                // a power of two at or below it, at least 2^-100; O is rescaled by an exact ratio
-                const float up = __uint_as_float(max(27u << 23, __float_as_uint(most) & 0x7f800000u));
+                // a power of two at or below it, within 2^-100 .. 2^126; O is rescaled by an exact ratio
+                const float up = __uint_as_float(min(253u << 23, max(27u << 23, __float_as_uint(most) & 0x7f800000u)));
                 if (up > G) {
-                    ratio = __fdiv_rn(G, up);
+                    ratio = __fmul_rn(G, __uint_as_float((254u << 23) - __float_as_uint(up)));
                     G = up;
                 }
             }
-            if (n >= KS && !warp_wait(&sh.free_k[st], (use - 1) & 1u)) {
-                dead = true;
-                continue;
+            const float vf = __fmul_rn(gv, __fmul_rn(kVTop, __uint_as_float((254u << 23) - __float_as_uint(G))));
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv) {
+                uint64_t *const full = kv ? &sh.full_v[st] : &sh.full_k[st];
+                if (n >= KS && !warp_wait(kv ? &sh.free_v[st] : &sh.free_k[st], (use - 1) & 1u)) {
+                    dead = true;
+                    break;
+                }
+                if (kv && lane == 0) {
+                    sh.tile[st].valid[warp - 8] = valid;
+                    if (warp == 8) sh.tile[st].ratio = ratio, sh.tile[st].G = G;
+                }
+                expand<kWide>(base + (kv ? C::kOffV : C::kOffK) + st * C::kParts * kOp, key, rec + kv * (kRecBytes / 8), th, tl,
+                              kv ? vf : fk);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
             }
-            expand<kWide>(base + C::kOffK + st * C::kParts * kOp, key, wk, th, tl, fk);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.full_k[st]);
-            if (n >= KS && !warp_wait(&sh.free_v[st], (use - 1) & 1u)) {
-                dead = true;
-                continue;
-            }
-            if (lane == 0) {
-                sh.tile[st].valid[warp - 8] = valid;
-                if (warp == 8) sh.tile[st].ratio = ratio, sh.tile[st].G = G;
-            }
-            expand<kWide>(base + C::kOffV + st * C::kParts * kOp, key, wv, th, tl, __fmul_rn(gv, __fdiv_rn(kVTop, G)));
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.full_v[st]);
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         ++segs;
-        n_tile += g.blind ? 0 : g.take;
+        n_tile += take;
         next_segment<kWide>(a, w, false);
     }
     return dead;
@@ -666,12 +655,12 @@ __device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned c
             if (!dead && lane == 0) {
 #pragma unroll
                 for (int pass = 0; pass < (kWide ? 3 : 1); ++pass) {
-                    const uint64_t qa = sw128_desc(q0 + blk * C::kParts * kOp + (pass == 2 ? kOp : 0)),
-                                   kd = sw128_desc(kb + (pass == 1 ? kOp : 0));
+                    const uint32_t qa = k_desc(q0 + blk * C::kParts * kOp + (pass == 2 ? kOp : 0)),
+                                   kd = k_desc(kb + (pass == 1 ? kOp : 0));
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         const uint32_t off = (uint32_t)((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
-                        mma_bf16(tmem + blk * 128, qa + off, kd + off, kIdescS, pass > 0 || ks > 0);
+                        mma_ss(tmem + blk * 128, qa + off, kd + off, kIdescS, pass > 0 || ks > 0);
                     }
                 }
                 mma_commit(&sh.s_done[blk]);
@@ -682,7 +671,7 @@ __device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned c
             if (!dead && lane == 0) {
 #pragma unroll
                 for (int pass = 0; pass < (kWide ? 3 : 1); ++pass) {
-                    const uint64_t vd = mn_desc(vb + (pass == 1 ? kOp : 0));
+                    const uint32_t vd = mn_desc(vb + (pass == 1 ? kOp : 0));
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         const uint32_t p = kWide ? tmem + C::kTmemP + 32 * (ks >> 1) + 8 * (ks & 1) + (pass == 2 ? 16 : 0)
@@ -758,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             cut->cut = 0;
             if (blockIdx.x == 0)
                 for (int b = 0; b < a.batch; ++b)
-                    if (__ldg(a.kv_len + b) > (a.pages_per_seq << a.pools.shift)) atomicOr(&g_fault, tq3::kFaultPoolIndex);
+                    if (__ldg(a.kv_len + b) > a.max_keys) atomicOr(&g_fault, tq3::kFaultPoolIndex);
         }
     }
     tc_fence_before();
