@@ -308,14 +308,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
         {
             constexpr int kEach = R / kWarps;
             float v[kEach][4];
+            int row[kEach];  // a row behind the last one repeats it, and counts as zeros
+#pragma unroll
+            for (int n = 0; n < kEach; ++n) row[n] = min(r0 + kWarps * n + warp, rows - 1);
+            load_rows<kEach, !kWide>(a, s, w.head, row, lane, v);
 #pragma unroll
             for (int n = 0; n < kEach; ++n) {
                 const int r = kWarps * n + warp;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[n][i] = 0.0f;
-                if (r0 + r < rows) load_row(a, s, w.head, r0 + r, lane, v[n]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[n][i] = __fmul_rn(v[n][i], sg[i]);
+                for (int i = 0; i < 4; ++i) v[n][i] = r0 + r < rows ? __fmul_rn(v[n][i], sg[i]) : 0.0f;
                 row_fwht(v[n], lane);
                 float m = fmaxf(fmaxf(fabsf(v[n][0]), fabsf(v[n][1])), fmaxf(fabsf(v[n][2]), fabsf(v[n][3])));
 #pragma unroll
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], f);
             if (whole) {
-                store_row(a, s, w.head, r0 + r, lane, sg, v);
+                store_row<!kWide>(a, s, w.head, r0 + r, lane, sg, v);
             } else {
                 *reinterpret_cast<float4 *>(slot + r * 128 + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
                 if (lane == 0) slot[R * 128 + r] = sum == 0.0f ? -INFINITY : m, slot[R * 129 + r] = sum;

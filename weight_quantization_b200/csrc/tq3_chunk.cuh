@@ -100,7 +100,13 @@ __device__ __forceinline__ Span block_span(const Args &a, const Seq &s, int bloc
     return span_of(a, before + token_of(a, r0), before + token_of(a, r1));
 }
 
-// A block without a visible key still counts one tile: its rows are written as zeros.
+// On the line a segment is kSetup units, what loading its queries and storing its results costs in tiles,
+// and then its tiles; who has the first tile begins it. A block without a visible key still counts one
+// tile: its rows are written as zeros.
+template <int R>
+__host__ __device__ constexpr int setup_units() {
+    return R == 8 ? 2 : 4;
+}
 template <int R>
 __device__ __forceinline__ int blocks_of(const Args &a, const Seq &s) {
     return (s.new_tokens * a.group + R - 1) / R;
@@ -109,7 +115,7 @@ template <int R>
 __device__ __forceinline__ int64_t tiles_of_head(const Args &a, const Seq &s) {
     int64_t n = 0;
 #pragma unroll 1
-    for (int i = blocks_of<R>(a, s) - 1; i >= 0; --i) n += max(1, block_span<R>(a, s, i).n);
+    for (int i = blocks_of<R>(a, s) - 1; i >= 0; --i) n += max(1, block_span<R>(a, s, i).n) + setup_units<R>();
     return n;
 }
 
@@ -155,8 +161,9 @@ constexpr int64_t workspace_bytes(int64_t ctas) {
 template <int R, int kThreads>
 struct Walk {
     Line line;
-    int64_t at, end;  // on the line
-    int b, head, block, blocks, tile;  // tile: the first one of the segment that is this CTA's
+    int64_t seg, end;  // on the line: the segment here, the end of the part
+    int b, head, block, blocks;
+    int tile, count;  // the segment's tiles that are this CTA's: the first one, how many
     Seq seq;
     Span span;
 
@@ -179,7 +186,8 @@ struct Walk {
             for (int w = 0; w < kWarps; ++w) total += scratch[w];
         }
         line = Line(min(total, int64_t(1) << 46), gridDim.x);
-        at = end = 0;
+        int64_t at = 0;
+        seg = end = 0;
         if ((int)blockIdx.x >= line.parts) return;
         at = line.begin(blockIdx.x);
         end = line.begin(blockIdx.x + 1);
@@ -233,43 +241,51 @@ struct Walk {
 #pragma unroll 1
         for (;; ++block) {
             span = block_span<R>(a, seq, block);
-            const int n = max(1, span.n);
+            const int n = max(1, span.n) + setup_units<R>();
             if (off < n) break;
             off -= n;
         }
-        tile = (int)off;
+        seg = at - off;
+        if (!settle(at)) next(a);
     }
-    __device__ __forceinline__ bool done() const { return at >= end; }
+    __device__ __forceinline__ bool done() const { return seg >= end; }
     __device__ __forceinline__ int segment() const { return max(1, span.n); }
-    __device__ __forceinline__ int take() const {
-        const int64_t n = segment() - tile, left = end - at;
-        return (int)(n < left ? n : left);
+    __device__ __forceinline__ int take() const { return count; }
+    // The tiles of the segment here from `at` on that are before the part's end; whether there are any.
+    __device__ __forceinline__ bool settle(int64_t at) {
+        const int64_t first = seg + setup_units<R>(), stop = min(first + segment(), end);
+        tile = (int)(max(at, first) - first);
+        count = (int)(stop - first) - tile;
+        return count > 0;
     }
     // Of the segment here, which this part begins and does not finish.
     __device__ __forceinline__ Cut cut_here() const {
         Cut c;
         c.cut = 1, c.n = 2;
-        const int64_t last = at + segment();
+        const int64_t last = seg + setup_units<R>() + segment();
 #pragma unroll 1
         for (int part = blockIdx.x + 2; part < line.parts && line.begin(part) < last; ++part) ++c.n;
         c.seq = b, c.head = head, c.block = block;
         return c;
     }
     __device__ __forceinline__ void next(const Args &a) {
-        at += take();
-        if (at >= end) return;
-        tile = 0;
-        if (++block == blocks) {
-            block = 0;
-            if (++head == a.pools.heads) {
-                head = 0;
-                do {
-                    seq = load_seq(a, ++b);
-                } while (seq.new_tokens == 0);
-                blocks = blocks_of<R>(a, seq);
+#pragma unroll 1
+        do {
+            seg += setup_units<R>() + segment();
+            if (seg >= end) return;
+            if (++block == blocks) {
+                block = 0;
+                if (++head == a.pools.heads) {
+                    head = 0;
+#pragma unroll 1
+                    do {
+                        seq = load_seq(a, ++b);
+                    } while (seq.new_tokens == 0);
+                    blocks = blocks_of<R>(a, seq);
+                }
             }
-        }
-        span = block_span<R>(a, seq, block);
+            span = block_span<R>(a, seq, block);
+        } while (!settle(seg));
     }
 };
 
@@ -302,33 +318,51 @@ __device__ __forceinline__ void lane_signs(const Args &a, int lane, float (&sg)[
 #pragma unroll
     for (int i = 0; i < 4; ++i) sg[i] = sign_of(a.mask, 4 * lane + i);
 }
-// Elements 4 l .. 4 l + 3 of row `row` of (sequence, head).
-__device__ __forceinline__ void load_row(const Args &a, const Seq &s, int head, int row, int lane, float (&v)[4]) {
-    const int token = token_of(a, row);
-    const int64_t at = (int64_t)(s.start + token) * a.q_token + (int64_t)(head * a.group + row - token * a.group) * a.q_head +
-                       4 * lane;
-    if (a.q_bf16) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + at));
-        v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+// Elements 4 l .. 4 l + 3 of N rows, row[n] of (sequence, head) each; kBf16: q is known to be bf16.
+template <int N, bool kBf16>
+__device__ __forceinline__ void load_rows(const Args &a, const Seq &s, int head, const int (&row)[N], int lane, float (&v)[N][4]) {
+    int64_t at[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int token = token_of(a, row[n]);
+        at[n] = (int64_t)(s.start + token) * a.q_token + (int64_t)(head * a.group + row[n] - token * a.group) * a.q_head + 4 * lane;
+    }
+    if (kBf16 || a.q_bf16) {
+        uint2 w[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) w[n] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + at[n]));
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            v[n][0] = bf16_lo(w[n].x), v[n][1] = bf16_hi(w[n].x), v[n][2] = bf16_lo(w[n].y), v[n][3] = bf16_hi(w[n].y);
     } else {
-        const float4 w = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at));
-        v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+        float4 w[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) w[n] = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + at[n]));
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n][0] = w[n].x, v[n][1] = w[n].y, v[n][2] = w[n].z, v[n][3] = w[n].w;
     }
 }
 
-// out = s . H(row) post, from the rotated basis.
-__device__ __forceinline__ void store_row(const Args &a, const Seq &s, int head, int row, int lane, const float (&sg)[4],
-                                          float (&v)[4]) {
-    row_fwht(v, lane);
+// Stores s . v post as a row of the result; store_row: of H(v), from the rotated basis.
+template <bool kBf16>
+__device__ __forceinline__ void put_row(const Args &a, const Seq &s, int head, int row, int lane, const float (&sg)[4],
+                                        float (&v)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(__fmul_rn(v[i], tq3::fwht_post()), sg[i]);
     const int token = token_of(a, row);
     const int64_t at = (((int64_t)(s.start + token) * a.pools.heads + head) * a.group + row - token * a.group) * 128 + 4 * lane;
-    if (a.out_bf16)
+    if (kBf16 || a.out_bf16)
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     else
         *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void store_row(const Args &a, const Seq &s, int head, int row, int lane, const float (&sg)[4],
+                                          float (&v)[4]) {
+    row_fwht(v, lane);
+    put_row<kBf16>(a, s, head, row, lane, sg, v);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -377,7 +411,7 @@ __device__ __forceinline__ void merge_cut(const Args &a) {
     }
     float sg[4];
     lane_signs(a, lane, sg);
-    store_row(a, s, c.head, row, lane, sg, v);
+    store_row<false>(a, s, c.head, row, lane, sg, v);
 }
 
 constexpr int kJoinThreads = 128;

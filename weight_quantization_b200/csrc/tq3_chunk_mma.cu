@@ -11,14 +11,14 @@
 // 2^-27 of the largest. A value whose factor is not finite becomes zero and poisons its key's logits
 // instead: a row that sees it gets NaN, any other is not touched.
 //
-// One CTA of 16 warps per SM. Warps 0-3 and 4-7 are the softmax of rows 0-127 and 128-255: a thread a row,
-// which lies in its tensor-memory lane. Warps 8-11 decode: a thread a key. Warp 12 issues the products; 13-15
-// fill its warpgroup.
-//     decode   records of the next tile into registers; indices to selectors of byte permutes, which
-//              fetch the bytes of four fp16 centroids at a time; times the factor (hi + lo); 16-byte
+// One CTA of 20 warps per SM. Warps 0-3 and 4-7 are the softmax of rows 0-127 and 128-255: a thread a row,
+// which lies in its tensor-memory lane. Warps 8-11 decode keys and 12-15 values: a thread a record. Warp 16
+// issues the products; 17-19 fill its warpgroup.
+//     decode   the eight centroids times the record's factor as a table of two bytes each; indices to the
+//              selectors of byte permutes, which fetch the bytes of four operands at a time; 16-byte
 //              chunks into the 128-byte-swizzled operand tile (K as K-major B, V as MN-major B)
-//     softmax  w = 2^(s - M) in one pass over S with the M that stood, redone with a larger one where a
-//              row passes it by 2^8 (O is rescaled then); P as fp16 over S's columns
+//     softmax  the maximum of a row of S; M is raised where it is passed by 2^8 (O is rescaled then);
+//              w = 2^(s - M), P as fp16 over S's columns that have been read
 //     issue    S0(0) S1(0) | P0(i) V(i) -> O0, S0(i+1) | P1(i) V(i) -> O1, S1(i+1) | ...
 // so that the tensor core works on one half of the rows while the other half's softmax runs. S(i+1) is
 // issued behind O(i), so a row whose S(i+1) has arrived may touch O. For fp32 queries or results the
@@ -46,15 +46,17 @@ namespace tq3_chunk_mma {
 using namespace tq3_chunk;
 
 constexpr int kBlock = 128;           // rows of a product
-constexpr int kThreads = 512;
-// registers a thread: 128 at launch; 256 softmax, 128 decode and 128 issue threads share the same 65536
-constexpr int kRegsSoftmax = 184, kRegsDecode = 104, kRegsIssue = 40;
-static_assert(256 * kRegsSoftmax + 128 * kRegsDecode + 128 * kRegsIssue <= kThreads * 128, "registers");
+constexpr int kThreads = 640;
+// registers a thread: 96 at launch; 256 softmax, 256 decode and 128 issue threads share the same 61440
+constexpr int kRegsSoftmax = 152, kRegsDecode = 72, kRegsIssue = 32;
+static_assert(256 * kRegsSoftmax + 256 * kRegsDecode + 128 * kRegsIssue <= kThreads * 96, "registers");
+constexpr int kIssueWarp = 16;
 constexpr int kBox = 128 * 128;       // 64 coordinates of a 128-row fp16 operand, in bytes
 constexpr int kOp = 2 * kBox;
 constexpr uint32_t kMaxPolls = 1u << 24;
 constexpr float kLazy = 8.0f, kLift = 6.0f;  // as in tq3_chunk.cu
-constexpr int kRecStages = 2, kRecBytes = 2 * kTileKeys * tq3_cache::kRec;
+constexpr int kRecBytes = kTileKeys * tq3_cache::kRec;  // a tile's records of one pool
+constexpr int kRecStages = 2;
 constexpr int kQBits = 7;             // a bound of |q~| of a segment is scaled to 2^7 .. 2^8
 constexpr float kVTop = 8192.0f;      // a value of factor G has this one
 
@@ -73,12 +75,11 @@ struct Cfg {
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + NB * kParts * kOp;
     static constexpr int kOffV = kOffK + KS * kParts * kOp;
-    static constexpr int kOffRec = kOffV + KS * kParts * kOp;  // a tile's key records, then its value records
-    static constexpr int kOffShared = kOffRec + kRecStages * kRecBytes;
-    static constexpr int kSmem = 1024 + kOffShared + 1024;
+    static constexpr int kOffRec = kOffV + KS * kParts * kOp;  // per stage: a tile's key and value records
+    static constexpr int kOffFac = kOffRec + kRecStages * 2 * kRecBytes;  // per stage and key: norm, scale of the value
+    static constexpr int kOffShared = kOffFac + kRecStages * kTileKeys * 8;
+    static constexpr int kSmem = 1024 + kOffShared + 1280;
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-    // centroids times kGain: see tq3_chunk.cu
-    static constexpr float kGain = kWide ? 1.0f : 1.6196665f;
     // tensor memory: S, O, and P (over S where two blocks fill the memory)
     static constexpr int kTmemO = NB * 128, kTmemP = kWide ? 256 : 0;
 };
@@ -98,7 +99,7 @@ struct Shared {
     Walk<256, kThreads> walk256;
     Walk<128, kThreads> walk128;
 };
-static_assert(sizeof(Shared) <= 1024, "shared block");
+static_assert(sizeof(Shared) <= 1280, "shared block");
 template <bool kWide>
 __device__ __forceinline__ Walk<Cfg<kWide>::R, kThreads> &walk_of(Shared &s);
 template <>
@@ -186,19 +187,17 @@ __device__ __forceinline__ void named_sync() {
     asm volatile("bar.sync %0, %1;" ::"n"(kBar), "n"(kCount) : "memory");
 }
 
-// Four fp16 centroids a selector: the low and the high bytes of the eight values, in two words each.
+// The eight centroids times a factor, rounded to fp16: their low and their high bytes, in two words each.
+// Magnitudes 0 .. 3 are indices 4 .. 7 and, negative, 3 .. 0.
 struct Table {
     uint32_t lo0, lo1, hi0, hi1;
 };
-__device__ __forceinline__ Table make_table(const uint16_t (&h)[8]) {
-    Table t = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        t.lo0 |= (uint32_t)(h[i] & 255) << (8 * i);
-        t.lo1 |= (uint32_t)(h[i + 4] & 255) << (8 * i);
-        t.hi0 |= (uint32_t)(h[i] >> 8) << (8 * i);
-        t.hi1 |= (uint32_t)(h[i + 4] >> 8) << (8 * i);
-    }
+__device__ __forceinline__ Table make_table(uint32_t m01, uint32_t m23) {
+    Table t;
+    t.lo1 = __byte_perm(m01, m23, 0x6420);
+    t.hi1 = __byte_perm(m01, m23, 0x7531);
+    t.lo0 = __byte_perm(m01, m23, 0x0246);
+    t.hi0 = __byte_perm(m01, m23, 0x1357) ^ 0x80808080u;
     return t;
 }
 __device__ __forceinline__ void four(const Table &t, uint32_t sel, uint32_t &a, uint32_t &b) {
@@ -214,13 +213,18 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t x) {
 }
 
 // The 128 centroids of a record's indices times a factor, into row `row` of an operand, 32 at a time (the
-// loop is kept small: the roles' loops share the instruction cache). hi + lo is the factor.
+// loop is kept small: the roles' loops share the instruction cache).
 template <bool kWide>
-__device__ __forceinline__ void expand(unsigned char *op, int row, const uint32_t *rec, const Table &th, const Table &tl,
-                                       float factor) {
-    const uint32_t fh = h2(factor, factor);
-    const float rest = __fsub_rn(factor, f2(fh).x);
-    const uint32_t fl = h2(rest, rest);
+__device__ __forceinline__ void expand(unsigned char *op, int row, const uint32_t *rec, float factor) {
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = __fmul_rn(tq3::centroid(4 + i), factor);
+    const uint32_t m01 = h2(m[0], m[1]), m23 = h2(m[2], m[3]);
+    const Table th = make_table(m01, m23);
+    Table tl = {};
+    if (kWide)
+        tl = make_table(h2(__fsub_rn(m[0], f2(m01).x), __fsub_rn(m[1], f2(m01).y)),
+                        h2(__fsub_rn(m[2], f2(m23).x), __fsub_rn(m[3], f2(m23).y)));
 #pragma unroll 1
     for (int part = 0; part < 4; ++part) {
         const uint32_t w0 = rec[3 * part], w1 = rec[3 * part + 1], w2 = rec[3 * part + 2];
@@ -229,26 +233,16 @@ __device__ __forceinline__ void expand(unsigned char *op, int row, const uint32_
         for (int c = 0; c < 4; ++c) {
             const uint32_t x = c == 0 ? w0 : c == 1 ? __funnelshift_r(w0, w1, 24) : c == 2 ? __funnelshift_r(w1, w2, 16) : w2 >> 8;
             const uint32_t sel = nibbles(x);
-            uint32_t ch[4], h[4];
-            four(th, sel, ch[0], ch[1]);
-            four(th, sel >> 16, ch[2], ch[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = mul_h2(ch[i], fh);
-            uint4 *const chunk = reinterpret_cast<uint4 *>(to + (((4 * (part & 1) + c) ^ (row & 7)) << 4));
+            unsigned char *const chunk = to + (((4 * (part & 1) + c) ^ (row & 7)) << 4);
+            uint4 h;
+            four(th, sel, h.x, h.y);
+            four(th, sel >> 16, h.z, h.w);
+            *reinterpret_cast<uint4 *>(chunk) = h;
             if (kWide) {
-                // hi = RN(ch fh); lo = (ch fh - hi) + ch fl + cl fh, the difference exact
-                uint32_t cl[4], l[4];
-                four(tl, sel, cl[0], cl[1]);
-                four(tl, sel >> 16, cl[2], cl[3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    l[i] = fma_h2(cl[i], fh, fma_h2(ch[i], fl, fma_h2(ch[i], fh, h[i] ^ 0x80008000u)));
-                *reinterpret_cast<uint4 *>(reinterpret_cast<unsigned char *>(chunk) + kOp) = make_uint4(l[0], l[1], l[2], l[3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = fma_h2(ch[i], fl, h[i]);
+                four(tl, sel, h.x, h.y);
+                four(tl, sel >> 16, h.z, h.w);
+                *reinterpret_cast<uint4 *>(chunk + kOp) = h;
             }
-            *chunk = make_uint4(h[0], h[1], h[2], h[3]);
         }
     }
 }
@@ -316,12 +310,18 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
         {
             // |q~| is at most the sum of |q| over a row, that is 32 times the largest sum over a lane
             float m = 0.0f;
-#pragma unroll 4
-            for (int r = 0; r < n_rows; ++r) {
-                float v[4];
-                load_row(a, g.s, g.head, wr + r, lane, v);
-                const float x = __fadd_rn(__fadd_rn(fabsf(v[0]), fabsf(v[1])), __fadd_rn(fabsf(v[2]), fabsf(v[3])));
-                m = x < INFINITY ? fmaxf(m, x) : m;  // a row that is not finite spoils only itself
+            float v[8][4];
+            int row[8];  // a row behind the last one repeats it, and counts as zeros
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 8) {  // eight rows at a time, so that their loads overlap
+#pragma unroll
+                for (int r = 0; r < 8; ++r) row[r] = min(wr + r0 + r, g.rows - 1);
+                load_rows<8, !kWide>(a, g.s, g.head, row, lane, v);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const float x = __fadd_rn(__fadd_rn(fabsf(v[r][0]), fabsf(v[r][1])), __fadd_rn(fabsf(v[r][2]), fabsf(v[r][3])));
+                    m = x < INFINITY ? fmaxf(m, x) : m;  // a row that is not finite spoils only itself
+                }
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -336,23 +336,26 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
             const float up = __uint_as_float((uint32_t)up_exp << 23);
             if (tid == 0) sh.down = __uint_as_float((uint32_t)(254 - up_exp) << 23);
             unsigned char *const op = base + C::kOffQ + blk * C::kParts * kOp + (lane >> 4) * kBox + 8 * (lane & 1);
-#pragma unroll 2
-            for (int r = 0; r < 32; ++r) {
-                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (r < n_rows) load_row(a, g.s, g.head, wr + r, lane, v);
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += 8) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], sg[i]);
-                row_fwht(v, lane);
+                for (int r = 0; r < 8; ++r) row[r] = min(wr + r0 + r, g.rows - 1);
+                load_rows<8, !kWide>(a, g.s, g.head, row, lane, v);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], up);
-                const int row = (warp & 3) * 32 + r;
-                unsigned char *const to = op + row * 128 + (((lane >> 1 & 7) ^ (row & 7)) << 4);
-                const uint2 hi = make_uint2(h2(v[0], v[1]), h2(v[2], v[3]));
-                *reinterpret_cast<uint2 *>(to) = hi;
-                if (kWide) {
-                    const float2 x = f2(hi.x), y = f2(hi.y);
-                    *reinterpret_cast<uint2 *>(to + kOp) =
-                        make_uint2(h2(__fsub_rn(v[0], x.x), __fsub_rn(v[1], x.y)), h2(__fsub_rn(v[2], y.x), __fsub_rn(v[3], y.y)));
+                for (int r = 0; r < 8; ++r) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[r][i] = r0 + r < n_rows ? __fmul_rn(v[r][i], sg[i]) : 0.0f;
+                    row_fwht(v[r], lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[r][i] = __fmul_rn(v[r][i], up);
+                    unsigned char *const to = op + ((warp & 3) * 32 + r0 + r) * 128 + (((lane >> 1 & 7) ^ r) << 4);
+                    const uint2 hi = make_uint2(h2(v[r][0], v[r][1]), h2(v[r][2], v[r][3]));
+                    *reinterpret_cast<uint2 *>(to) = hi;
+                    if (kWide) {
+                        const float2 x = f2(hi.x), y = f2(hi.y);
+                        *reinterpret_cast<uint2 *>(to + kOp) = make_uint2(h2(__fsub_rn(v[r][0], x.x), __fsub_rn(v[r][1], x.y)),
+                                                                          h2(__fsub_rn(v[r][2], y.x), __fsub_rn(v[r][3], y.y)));
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -463,7 +466,7 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
         // the rows: finished, or a part of a cut segment. Their sums pass through shared memory (Q and K:
         // every S product is done) from a thread a row to a warp a row
         if (n_rows > 0 && !dead) {
-            const float f = g.blind || sum == 0.0f ? 0.0f : __fmul_rn(__frcp_rn(sum), __fmul_rn(G, 1.0f / (kVTop * C::kGain)));
+            const float f = g.blind || sum == 0.0f ? 0.0f : __fmul_rn(__frcp_rn(sum), __fmul_rn(G, 1.0f / kVTop));
             unsigned char *const stage = base + C::kOffQ + warp * 16384;
             if (!g.blind) {
 #pragma unroll 1
@@ -479,18 +482,31 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
                 __syncwarp();
             }
             float *const slot = slot_at<R>(a, gridDim.x, 2 * blockIdx.x + (g.first == 0));
-#pragma unroll 2
-            for (int r = 0; r < n_rows; ++r) {
-                const float fr = __shfl_sync(0xffffffffu, f, r);
-                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (fr != 0.0f) {
-                    const float4 x = *reinterpret_cast<const float4 *>(stage + 512 * r + ((lane ^ r) << 4));
-                    v[0] = __fmul_rn(x.x, fr), v[1] = __fmul_rn(x.y, fr), v[2] = __fmul_rn(x.z, fr), v[3] = __fmul_rn(x.w, fr);
+            const bool whole = g.whole;
+#pragma unroll 1
+            for (int r0 = 0; r0 < n_rows; r0 += 4) {
+                float v[4][4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float fr = __shfl_sync(0xffffffffu, f, r0 + r);
+                    const float4 x = *reinterpret_cast<const float4 *>(stage + 512 * (r0 + r) + ((lane ^ (r0 + r)) << 4));
+                    v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[r][i] = fr == 0.0f ? 0.0f : __fmul_rn(v[r][i], fr);
                 }
-                if (g.whole)
-                    store_row(a, g.s, g.head, wr + r, lane, sg, v);
-                else
-                    *reinterpret_cast<float4 *>(slot + (32 * warp + r) * 128 + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
+                if (whole) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) row_fwht(v[r], lane);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r0 + r < n_rows) {
+                        if (whole)
+                            put_row<!kWide>(a, g.s, g.head, wr + r0 + r, lane, sg, v[r]);
+                        else
+                            *reinterpret_cast<float4 *>(slot + (32 * warp + r0 + r) * 128 + 4 * lane) =
+                                make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
+                    }
             }
             if (!g.whole && lane < n_rows) {
                 slot[R * 128 + 32 * warp + lane] = sum == 0.0f ? -INFINITY : M;
@@ -507,32 +523,23 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const uint8_t *src, uint
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Warps 8 .. 11: a thread a key, of both pools.
+// Warps 8 .. 11 decode the keys and 12 .. 15 the values: a thread a record.
 template <bool kWide>
 __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned char *base) {
     using C = Cfg<kWide>;
     constexpr int KS = C::KS, R = C::R;
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, key = tid - 256;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, key = tid & 127;
+    const bool values = warp >= 12;  // (one copy of the code for both)
+    unsigned char *const recs = base + C::kOffRec + (values ? kRecBytes : 0), *const ops = base + (values ? C::kOffV : C::kOffK);
+    uint64_t *const full = values ? sh.full_v : sh.full_k, *const free = values ? sh.free_v : sh.free_k;
+    const uint8_t *const pool = values ? a.pools.v : a.pools.k;
     bool dead = false;
     uint32_t n_tile = 0, segs = 0;
-    Table th, tl;
-    {
-        uint16_t hh[8], hl[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = __fmul_rn(tq3::centroid(i), C::kGain);
-            const uint32_t p = h2(x, 0.0f);
-            hh[i] = (uint16_t)p;
-            hl[i] = (uint16_t)h2(__fsub_rn(x, f2(p).x), 0.0f);
-        }
-        th = make_table(hh);
-        tl = make_table(hl);
-    }
     while (!w.done()) {
         const Segment<kWide> g(a, w);
         const int take = g.blind ? 0 : g.take;
-        // Two steps ahead of a tile its page entry is asked for, one step ahead its records. -1: no row
+        // Two steps ahead of a tile its page entry is asked for, one step ahead its record. -1: no row
         // needs this thread's key (of no tile, or behind a window); -2: an entry outside the pool.
         int32_t entry = -1;
         uint32_t have = 0;  // bit i % kRecStages: the key of tile i has a page
@@ -546,7 +553,7 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
                 }
             }
         };
-        auto fetch = [&](int i) {  // the records of tile i, whose entry is in hand
+        auto fetch = [&](int i) {  // the record of tile i, whose entry is in hand
             const uint32_t bit = 1u << (i % kRecStages);
             have &= ~bit;
             if (i < take) {
@@ -555,13 +562,13 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
                 if (entry != -1 && !ok) atomicOr(&g_fault, tq3::kFaultPoolIndex);
                 if (ok) have |= bit;
                 const int64_t at = ok ? tq3_cache::record_at(a.pools, entry, g.head, j & ((1 << a.pools.shift) - 1)) : 0;
-                const uint32_t to = smem_u32(base + C::kOffRec + (i % kRecStages) * kRecBytes) + key * tq3_cache::kRec;
+                const uint32_t to = smem_u32(recs + (i % kRecStages) * 2 * kRecBytes) + key * tq3_cache::kRec;
                 const uint32_t bytes = ok ? 8 : 0;  // nothing is read for 0 bytes, zeros are written
+                const uint8_t *const from = pool + at;
 #pragma unroll
-                for (int x = 0; x < 7; ++x) {
-                    cp_async8(to + 8 * x, a.pools.k + at + 8 * x, bytes);
-                    cp_async8(to + kRecBytes / 2 + 8 * x, a.pools.v + at + 8 * x, bytes);
-                }
+                for (int x = 0; x < 7; ++x) cp_async8(to + 8 * x, from + 8 * x, bytes);
+                if (!values)
+                    cp_async8(smem_u32(base + C::kOffFac + (i % kRecStages) * kTileKeys * 8) + key * 8, a.pools.v + at + 48, bytes);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -569,61 +576,65 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
         ask(0);
         fetch(0);
         ask(1);
-        if (take > 0 && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
-        const float coef = __fmul_rn(__fmul_rn(a.coef, 1.0f / C::kGain), sh.down);
+        if (!values && take > 0 && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
+        const float coef = __fmul_rn(a.coef, sh.down);
 #pragma unroll 1
         for (int i = 0; i < take; ++i) {
             const uint32_t n = n_tile + i, st = n % KS, use = n / KS;
             fetch(i + 1);
             ask(i + 2);
             asm volatile("cp.async.wait_group 1;" ::: "memory");  // a thread reads only what it copied
-            const uint32_t *const rec =
-                reinterpret_cast<const uint32_t *>(base + C::kOffRec + (i % kRecStages) * kRecBytes + key * tq3_cache::kRec);
-            const float2 rk = *reinterpret_cast<const float2 *>(rec + 12),
-                         rv = *reinterpret_cast<const float2 *>(rec + kRecBytes / 8 + 12);
-            float fk = __fmul_rn(__fmul_rn(rk.x, rk.y), coef), gv = __fmul_rn(rv.x, rv.y);
-            if (!(fabsf(gv) < INFINITY)) fk = __uint_as_float(0x7fffffffu), gv = 0.0f;
-            // the largest factor of the tile (the four warps leave together: a warp whose wait ran out
-            // says so here)
-            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(gv)));
-            const uint32_t valid = __ballot_sync(0xffffffffu, (have >> (i % kRecStages)) & 1u);
-            if (lane == 0) sh.gmax[n & 1][warp - 8] = dead ? 0xffffffffu : top;
-            named_sync<2, 128>();
-            uint32_t all = 0;
+            const uint32_t *const rec = reinterpret_cast<const uint32_t *>(
+                recs + (i % kRecStages) * 2 * kRecBytes + key * tq3_cache::kRec);
+            const float2 own = *reinterpret_cast<const float2 *>(rec + 12);
+            float factor = __fmul_rn(own.x, own.y);
+            if (values) {
+                if (!(fabsf(factor) < INFINITY)) factor = 0.0f;
+                // the largest factor of the tile (the four warps leave together: a warp whose wait ran
+                // out says so here)
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(factor)));
+                if (lane == 0) sh.gmax[n & 1][warp & 3] = dead ? 0xffffffffu : top;
+                named_sync<2, 128>();
+                uint32_t all = 0;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) all = max(all, sh.gmax[n & 1][x]);
-            if (all == 0xffffffffu) {
-                dead = true;
-                break;
-            }
-            const float most = __uint_as_float(all);
-            float ratio = 1.0f;
-            if (G == 0.0f || most > 4.0f * G) {
-                // a power of two at or below it, within 2^-100 .. 2^126; O is rescaled by an exact ratio
-                const float up = __uint_as_float(min(253u << 23, max(27u << 23, __float_as_uint(most) & 0x7f800000u)));
-                if (up > G) {
-                    ratio = __fmul_rn(G, __uint_as_float((254u << 23) - __float_as_uint(up)));
-                    G = up;
-                }
-            }
-            const float vf = __fmul_rn(gv, __fmul_rn(kVTop, __uint_as_float((254u << 23) - __float_as_uint(G))));
-#pragma unroll 1
-            for (int kv = 0; kv < 2; ++kv) {
-                uint64_t *const full = kv ? &sh.full_v[st] : &sh.full_k[st];
-                if (n >= KS && !warp_wait(kv ? &sh.free_v[st] : &sh.free_k[st], (use - 1) & 1u)) {
+                for (int x = 0; x < 4; ++x) all = max(all, sh.gmax[n & 1][x]);
+                if (all == 0xffffffffu) {
                     dead = true;
                     break;
                 }
-                if (kv && lane == 0) {
-                    sh.tile[st].valid[warp - 8] = valid;
-                    if (warp == 8) sh.tile[st].ratio = ratio, sh.tile[st].G = G;
+                const float most = __uint_as_float(all);
+                float ratio = 1.0f;
+                if (G == 0.0f || most > 4.0f * G) {
+                    // a power of two at or below it, within 2^-100 .. 2^126; O is rescaled by an exact ratio
+                    const float up = __uint_as_float(min(253u << 23, max(27u << 23, all & 0x7f800000u)));
+                    if (up > G) {
+                        ratio = __fmul_rn(G, __uint_as_float((254u << 23) - __float_as_uint(up)));
+                        G = up;
+                    }
                 }
-                expand<kWide>(base + (kv ? C::kOffV : C::kOffK) + st * C::kParts * kOp, key, rec + kv * (kRecBytes / 8), th, tl,
-                              kv ? vf : fk);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full);
+                factor = __fmul_rn(factor, __fmul_rn(kVTop, __uint_as_float((254u << 23) - __float_as_uint(G))));
+                const uint32_t valid = __ballot_sync(0xffffffffu, (have >> (i % kRecStages)) & 1u);
+                if (n >= KS && !warp_wait(&free[st], (use - 1) & 1u)) {
+                    dead = true;
+                    continue;
+                }
+                if (lane == 0) {
+                    sh.tile[st].valid[warp & 3] = valid;
+                    if (warp == 12) sh.tile[st].ratio = ratio, sh.tile[st].G = G;
+                }
+            } else {
+                const float2 other = *reinterpret_cast<const float2 *>(base + C::kOffFac + (i % kRecStages) * kTileKeys * 8 + key * 8);
+                factor = __fmul_rn(factor, coef);
+                if (!(fabsf(__fmul_rn(other.x, other.y)) < INFINITY)) factor = __uint_as_float(0x7fffffffu);
+                if (dead || (n >= KS && !warp_wait(&free[st], (use - 1) & 1u))) {
+                    dead = true;
+                    break;
+                }
             }
+            expand<kWide>(ops + st * C::kParts * kOp, key, rec, factor);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         ++segs;
@@ -633,81 +644,88 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
     return dead;
 }
 
-// Warp 12.
+// The same value in every lane, so that the compiler keeps it in a uniform register: the tensor-core
+// instructions take their operands from those, and moving each there costs more than the product.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
+
+// Warp 16.
 template <bool kWide>
-__device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned char *base, uint32_t tmem) {
+__device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned char *base, uint32_t tmem_) {
     using C = Cfg<kWide>;
-    constexpr int NB = C::NB, KS = C::KS, R = C::R;
+    constexpr int KS = C::KS, R = C::R, kPasses = kWide ? 3 : 1;
+    constexpr uint32_t kBlockOp = C::kParts * kOp >> 4, kLo = kOp >> 4;  // in units of a descriptor's address
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
-    const int lane = threadIdx.x & 31;
     bool dead = false;
-    uint32_t n_tile = 0, segs = 0, n_blk[NB] = {};  // n_blk: S products of a block
+    uint32_t n_tile = 0, segs = 0, n_s0 = 0, n_s1 = 0;  // n_s: S products of a block
+    const uint32_t tmem = uniform(tmem_), at = uniform(smem_u32(base));
+    const uint32_t q0 = k_desc(at + C::kOffQ), k0 = k_desc(at + C::kOffK), v0 = mn_desc(at + C::kOffV);
     while (!w.done()) {
         const Segment<kWide> g(a, w);
-        if (!g.blind && !dead && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
-        const uint32_t q0 = smem_u32(base + C::kOffQ);
-        auto wait_op = [&](uint64_t *bar, uint32_t phase) {
-            if (!dead && !warp_wait(bar, phase)) dead = true;
-            tc_fence_after();
-        };
-        auto issue_s = [&](int blk, uint32_t n) {
-            const uint32_t kb = smem_u32(base + C::kOffK + (n % KS) * C::kParts * kOp);
-            if (!dead && lane == 0) {
-#pragma unroll
-                for (int pass = 0; pass < (kWide ? 3 : 1); ++pass) {
-                    const uint32_t qa = k_desc(q0 + blk * C::kParts * kOp + (pass == 2 ? kOp : 0)),
-                                   kd = k_desc(kb + (pass == 1 ? kOp : 0));
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t off = (uint32_t)((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
-                        mma_ss(tmem + blk * 128, qa + off, kd + off, kIdescS, pass > 0 || ks > 0);
+        const uint32_t take = uniform(g.blind ? 0 : g.take), nb = uniform(g.nb);
+        if (take > 0 && !dead && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
+#pragma unroll 1
+        for (uint32_t i = 0; i <= take && take > 0 && !dead; ++i) {
+            const uint32_t n = n_tile + i, st = n % KS, before = (n - 1) % KS;
+#pragma unroll 1
+            for (uint32_t blk = 0; blk < nb; ++blk) {
+                if (i > 0) {  // O of tile i - 1
+                    if ((blk == 0 && !warp_wait(&sh.full_v[before], ((n - 1) / KS) & 1u)) ||
+                        !warp_wait(&sh.p_ready[blk], ((blk ? n_s1 : n_s0) - 1) & 1u)) {
+                        dead = true;
+                        break;
                     }
-                }
-                mma_commit(&sh.s_done[blk]);
-            }
-        };
-        auto issue_o = [&](int blk, uint32_t n, bool first) {
-            const uint32_t vb = smem_u32(base + C::kOffV + (n % KS) * C::kParts * kOp);
-            if (!dead && lane == 0) {
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t d = tmem + C::kTmemO + blk * 128, p0 = tmem + C::kTmemP + blk * 128;
 #pragma unroll
-                for (int pass = 0; pass < (kWide ? 3 : 1); ++pass) {
-                    const uint32_t vd = mn_desc(vb + (pass == 1 ? kOp : 0));
+                        for (int ps = 0; ps < kPasses; ++ps) {
+                            const uint32_t v = v0 + before * kBlockOp + (ps == 1 ? kLo : 0);
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t p = kWide ? tmem + C::kTmemP + 32 * (ks >> 1) + 8 * (ks & 1) + (pass == 2 ? 16 : 0)
-                                                 : tmem + C::kTmemP + blk * 128 + 8 * ks;
-                        mma_ts(tmem + C::kTmemO + blk * 128, p, vd + (uint32_t)(ks * 2048 >> 4), kIdescO,
-                               !first || pass > 0 || ks > 0);
-                    }
-                }
-            }
-        };
-        if (!g.blind) {
-            for (int i = 0; i <= g.take && !dead; ++i) {
-                const uint32_t n = n_tile + i;
-#pragma unroll
-                for (int blk = 0; blk < NB; ++blk) {
-                    if (blk >= g.nb) break;
-                    if (i > 0) {  // O of tile i - 1
-                        if (blk == 0) wait_op(&sh.full_v[(n - 1) % KS], ((n - 1) / KS) & 1u);
-                        wait_op(&sh.p_ready[blk], (n_blk[blk] - 1) & 1u);
-                        issue_o(blk, n - 1, i == 1);
-                        if (!dead && lane == 0) {
-                            if (blk == g.nb - 1) mma_commit(&sh.free_v[(n - 1) % KS]);
-                            if (i == g.take) mma_commit(&sh.o_done[blk]);
+                            for (int ks = 0; ks < 8; ++ks)
+                                mma_ts(d, p0 + (kWide ? 32 * (ks >> 1) + 8 * (ks & 1) + (ps == 2 ? 16 : 0) : 8 * ks),
+                                       v + ks * (2048 >> 4), kIdescO, i > 1 || ps > 0 || ks > 0);
                         }
+                        if (blk == nb - 1) mma_commit(&sh.free_v[before]);
+                        if (i == take) mma_commit(&sh.o_done[blk]);
                     }
-                    if (i < g.take) {
-                        if (blk == 0) wait_op(&sh.full_k[n % KS], (n / KS) & 1u);
-                        issue_s(blk, n);
-                        if (!dead && lane == 0 && blk == g.nb - 1) mma_commit(&sh.free_k[n % KS]);
-                        ++n_blk[blk];
+                    __syncwarp();
+                }
+                if (i < take) {
+                    if (blk == 0) {
+                        if (!warp_wait(&sh.full_k[st], (n / KS) & 1u)) {
+                            dead = true;
+                            break;
+                        }
+                        tc_fence_after();
                     }
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ps = 0; ps < kPasses; ++ps) {
+                            const uint32_t q = q0 + blk * kBlockOp + (ps == 2 ? kLo : 0), k = k0 + st * kBlockOp + (ps == 1 ? kLo : 0);
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks) {
+                                const uint32_t off = (uint32_t)((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
+                                mma_ss(tmem + blk * 128, q + off, k + off, kIdescS, ps > 0 || ks > 0);
+                            }
+                        }
+                        mma_commit(&sh.s_done[blk]);
+                        if (blk == nb - 1) mma_commit(&sh.free_k[st]);
+                    }
+                    __syncwarp();
+                    if (blk)
+                        ++n_s1;
+                    else
+                        ++n_s0;
                 }
             }
         }
         ++segs;
-        n_tile += g.blind ? 0 : g.take;
+        n_tile += take;
         next_segment<kWide>(a, w, false);
     }
     return dead;
@@ -735,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         mbar_init(&sh.q_ready, 4 * NB);
         mbar_init(&sh.drain, 1);
     }
-    if (warp == 12) tmem_alloc(&sh.tmem, 512);
+    if (warp == kIssueWarp) tmem_alloc(&sh.tmem, 512);
     pdl_wait();
     Cut *const cut = reinterpret_cast<Cut *>(a.ws + (int64_t)blockIdx.x * kCutBytes);
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
@@ -762,25 +780,25 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             dead = softmax_role<kWide>(a, sh, base, tmem);
         else
             while (!w.done()) next_segment<kWide>(a, w, false);
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
         dead = decode_role<kWide>(a, sh, base);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (warp == 12)
+        if (warp == kIssueWarp)
             dead = issue_role<kWide>(a, sh, base, tmem);
         else
             while (!w.done()) next_segment<kWide>(a, w, false);
     }
     pdl_trigger();
     // products still in flight after a wait ran out get a bounded chance to finish
-    if (warp == 12 && dead && lane == 0) {
+    if (warp == kIssueWarp && dead && lane == 0) {
         mma_commit(&sh.drain);
         mbar_wait_bounded(&sh.drain, 0, kMaxPolls);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kIssueWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
