@@ -121,6 +121,8 @@ def sign_mask_words(sign_bits) -> np.ndarray:
 
 
 def _mask_arg(mask) -> np.ndarray:
+    if type(mask) is np.ndarray and mask.dtype == np.uint32 and mask.shape == (4,) and mask.flags.c_contiguous:
+        return mask
     m = np.ascontiguousarray(np.asarray(mask, dtype=np.uint32))
     if m.shape != (4,):
         raise ValueError("sign mask must be 4 uint32 words")
@@ -321,40 +323,73 @@ def tq3_attention_paged(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
 
 def _rows128(t, name: str):
     """[tokens, heads, 128] rows that may be a slice of a wider tensor: the last axis dense, the other
-    strides multiples of 16 bytes. Returns (pointer, token stride, head stride) in elements."""
+    strides multiples of 16 bytes. Returns (pointer, tokens, heads, token stride, head stride), the
+    strides in elements."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in _DT:
         raise ValueError(f"{name} must be float32 or bfloat16")
     if t.ndim != 3 or t.shape[2] != 128:
         raise ValueError(f"{name} must be [tokens, heads, 128]")
+    (tokens, heads, _), (token, head, last), ptr = t.shape, t.stride(), t.data_ptr()
     # the stride of an axis of one element is never used
-    token = t.stride(0) if t.shape[0] > 1 else 0
-    head = t.stride(1) if t.shape[1] > 1 else 0
-    if t.numel() and (t.stride(2) != 1 or token * t.element_size() % 16 or head * t.element_size() % 16
-                      or t.data_ptr() % 16):
+    if tokens <= 1:
+        token = 0
+    if heads <= 1:
+        head = 0
+    if tokens and heads and (last != 1 or (token | head) * t.element_size() % 16 or ptr % 16):
         raise ValueError(f"{name} must have dense rows that start on multiples of 16 bytes")
-    return t.data_ptr(), token, head
+    return ptr, tokens, heads, token, head
 
 
-def _cache_pools(k_pool, v_pool, device):
-    """Checks the pools of a batch's cache; returns (n_pages, kv_heads, page_size)."""
-    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-        _on(t, device, name, (torch.uint8,))
-        if t.ndim != 4 or t.shape[3] != 56:
-            raise ValueError(f"{name} must be uint8 [n_pages, kv_heads, page_size, 56]")
-        if t.data_ptr() % 16:
-            raise ValueError(f"{name} must start on a multiple of 16 bytes")
-    if k_pool.shape != v_pool.shape:
+def _at(t, index: int, name: str, dtype) -> int:
+    """Pointer of a contiguous tensor of this dtype on CUDA device `index`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _cache_pools(k_pool, v_pool, index: int):
+    """Checks the pools of a batch's cache; returns (k pointer, v pointer, n_pages, kv_heads, page_size)."""
+    kp, vp = _at(k_pool, index, "k_pool", torch.uint8), _at(v_pool, index, "v_pool", torch.uint8)
+    shape = k_pool.shape
+    if len(shape) != 4 or shape[3] != 56:
+        raise ValueError("k_pool must be uint8 [n_pages, kv_heads, page_size, 56]")
+    if shape != v_pool.shape:
         raise ValueError("k_pool and v_pool must have the same shape")
-    return k_pool.shape[:3]
+    if (kp | vp) % 16:
+        raise ValueError("k_pool and v_pool must start on multiples of 16 bytes")
+    return kp, vp, shape[0], shape[1], shape[2]
 
 
-def _cache_table(page_table, device):
-    _on(page_table, device, "page_table", (torch.int32,))
+def _cache_table(page_table, index: int):
+    ptr = _at(page_table, index, "page_table", torch.int32)
     if page_table.ndim != 2:
         raise ValueError("page_table must be int32 [batch, pages_per_seq]")
-    return page_table.shape
+    return (ptr, *page_table.shape)
+
+
+def _ints(t, index: int, name: str, n: int, dtype=torch.int32) -> int:
+    ptr = _at(t, index, name, dtype)
+    if t.numel() != n:
+        raise ValueError(f"{name} must be {dtype} [{n}]")
+    return ptr
+
+
+def _mask_bytes(mask) -> bytes:
+    return _mask_arg(mask).tobytes()
+
+
+def _on_device(index: int, call, *args) -> int:
+    """call(*args, the current stream of device `index`) with that device current."""
+    if index == torch.cuda.current_device():
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def tq3_cache_append(k: torch.Tensor, v: torch.Tensor, sign_mask, slots: torch.Tensor, k_pool: torch.Tensor,
@@ -364,22 +399,19 @@ def tq3_cache_append(k: torch.Tensor, v: torch.Tensor, sign_mask, slots: torch.T
     Token t goes to place slots[t] % page_size of page slots[t] // page_size (int64; a negative slot
     skips the token, one outside the pool is skipped and raises device fault bit 6; slots are distinct).
     Indices near a boundary are decided in fp64. Returns (k_pool, v_pool)."""
-    kp, k_token, k_head = _rows128(k, "k")
-    vp, v_token, v_head = _rows128(v, "v")
-    if k.shape != v.shape or k.dtype != v.dtype:
+    kp, tokens, heads, k_token, k_head = _rows128(k, "k")
+    vp, v_tokens, v_heads, v_token, v_head = _rows128(v, "v")
+    index = k.get_device()
+    if tokens != v_tokens or heads != v_heads or k.dtype != v.dtype:
         raise ValueError("k and v must have the same shape and dtype")
-    _on(v, k.device, "v")
-    n_pages, heads, page_size = _cache_pools(k_pool, v_pool, k.device)
-    if k.shape[1] != heads:
+    if v.get_device() != index:
+        raise ValueError(f"v must be on cuda:{index}")
+    k_pp, v_pp, n_pages, pool_heads, page_size = _cache_pools(k_pool, v_pool, index)
+    if heads != pool_heads:
         raise ValueError("k and v must have the pools' heads")
-    _on(slots, k.device, "slots", (torch.int64,))
-    if slots.numel() != k.shape[0]:
-        raise ValueError("slots must be int64 with one entry per token")
-    m = _mask_arg(sign_mask)
-    with torch.cuda.device(k.device):
-        st = lib().tq3_cache_append(kp, vp, _DT[k.dtype], k.shape[0], heads, k_token, k_head, v_token, v_head,
-                                    m.ctypes.data, _dev(slots, "slots"), _dev(k_pool, "k_pool"),
-                                    _dev(v_pool, "v_pool"), n_pages, page_size, _stream(k.device))
+    st = _on_device(index, lib().tq3_cache_append, kp, vp, _DT[k.dtype], tokens, heads, k_token, k_head, v_token, v_head,
+                    _mask_bytes(sign_mask), _ints(slots, index, "slots", tokens, torch.int64), k_pp, v_pp, n_pages,
+                    page_size)
     _check("tq3_cache_append", st)
     return k_pool, v_pool
 
@@ -393,29 +425,25 @@ def tq3_cache_read(k_pool: torch.Tensor, v_pool: torch.Tensor, page_table: torch
     bit 6. Returns (k_out, v_out)."""
     if not isinstance(k_pool, torch.Tensor) or not k_pool.is_cuda:
         raise ValueError("k_pool must be a CUDA tensor")
-    device = k_pool.device
-    n_pages, heads, page_size = _cache_pools(k_pool, v_pool, device)
-    batch, pages_per_seq = _cache_table(page_table, device)
-    _on(seq_start, device, "seq_start", (torch.int32,))
-    if seq_start.numel() != batch + 1:
-        raise ValueError("seq_start must be int32 [batch + 1]")
+    index = k_pool.get_device()
+    kp, vp, n_pages, heads, page_size = _cache_pools(k_pool, v_pool, index)
+    table, batch, pages_per_seq = _cache_table(page_table, index)
+    start = _ints(seq_start, index, "seq_start", batch + 1)
     if n_tokens < 0:
         raise ValueError("n_tokens must not be negative")
+    dtype = out_dtype if k_out is None else k_out.dtype
+    if dtype not in _DT:
+        raise ValueError("k_out and v_out must be float32 or bfloat16")
+    shape = (n_tokens, heads, 128)
     if k_out is None:
-        k_out = torch.empty((n_tokens, heads, 128), dtype=out_dtype, device=device)
+        k_out = k_pool.new_empty(shape, dtype=dtype)
     if v_out is None:
-        v_out = torch.empty((n_tokens, heads, 128), dtype=k_out.dtype, device=device)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _on(t, device, name, (torch.float32, torch.bfloat16))
-        _fits(t, n_tokens * heads * 128, name)
-    if k_out.dtype != v_out.dtype:
-        raise ValueError("k_out and v_out must have the same dtype")
-    m = _mask_arg(sign_mask)
-    with torch.cuda.device(device):
-        st = lib().tq3_cache_read(_dev(k_pool, "k_pool"), _dev(v_pool, "v_pool"), n_pages, heads, page_size,
-                                  _dev(page_table, "page_table"), batch, pages_per_seq, _dev(seq_start, "seq_start"),
-                                  n_tokens, m.ctypes.data, _dev(k_out, "k_out"), _dev(v_out, "v_out"),
-                                  _DT[k_out.dtype], _stream(device))
+        v_out = k_pool.new_empty(shape, dtype=dtype)
+    ko, vo = _at(k_out, index, "k_out", dtype), _at(v_out, index, "v_out", dtype)
+    _fits(k_out, n_tokens * heads * 128, "k_out")
+    _fits(v_out, n_tokens * heads * 128, "v_out")
+    st = _on_device(index, lib().tq3_cache_read, kp, vp, n_pages, heads, page_size, table, batch, pages_per_seq, start,
+                    n_tokens, _mask_bytes(sign_mask), ko, vo, _DT[dtype])
     _check("tq3_cache_read", st)
     return k_out, v_out
 
@@ -432,31 +460,25 @@ def tq3_attention_chunk(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Ten
     sequence has at most (default: all of q). Tokens that see no key get zeros, rows of no sequence are left as
     they were, keys without a page in the pool are masked out and raise device fault bit 6. Returns out
     [tokens, q_heads, 128]."""
-    qp, q_token, q_head = _rows128(q, "q")
-    n_pages, heads, page_size = _cache_pools(k_pool, v_pool, q.device)
-    tokens, q_heads = q.shape[:2]
+    qp, tokens, q_heads, q_token, q_head = _rows128(q, "q")
+    index = q.get_device()
+    kp, vp, n_pages, heads, page_size = _cache_pools(k_pool, v_pool, index)
     if heads < 1 or q_heads < heads or q_heads % heads:
         raise ValueError("q's heads must be a multiple of the pools' heads")
-    batch, pages_per_seq = _cache_table(page_table, q.device)
-    for name, t, n in (("q_start", q_start, batch + 1), ("kv_len", kv_len, batch)):
-        _on(t, q.device, name, (torch.int32,))
-        if t.numel() != n:
-            raise ValueError(f"{name} must be int32 [{n}]")
+    table, batch, pages_per_seq = _cache_table(page_table, index)
     if out is None:
-        out = torch.empty((tokens, q_heads, 128), dtype=out_dtype or q.dtype, device=q.device)
-    _on(out, q.device, "out", _DT)
+        out = q.new_empty((tokens, q_heads, 128), dtype=out_dtype or q.dtype)
+    if out.dtype not in _DT:
+        raise ValueError("out must be float32 or bfloat16")
+    op = _at(out, index, "out", out.dtype)
     _fits(out, tokens * q_heads * 128, "out")
     most = tokens if max_q is None else int(max_q)
-    m = _mask_arg(sign_mask)
-    with torch.cuda.device(q.device):
-        need = max(int(lib().tq3_attention_chunk_workspace(most, q_heads // heads)), 0)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        st = lib().tq3_attention_chunk(qp, _DT[q.dtype], tokens, q_heads, q_token, q_head, _dev(k_pool, "k_pool"),
-                                       _dev(v_pool, "v_pool"), n_pages, heads, page_size,
-                                       _dev(page_table, "page_table"), batch, pages_per_seq, _dev(q_start, "q_start"),
-                                       _dev(kv_len, "kv_len"), most, int(window), int(sinks), m.ctypes.data,
-                                       float(softmax_scale), _dev(out, "out"), _DT[out.dtype], ws.data_ptr(), need,
-                                       _stream(q.device))
+    need = max(int(lib().tq3_attention_chunk_workspace(most, q_heads // heads)), 0)
+    ws = k_pool.new_empty(need)
+    st = _on_device(index, lib().tq3_attention_chunk, qp, _DT[q.dtype], tokens, q_heads, q_token, q_head, kp, vp, n_pages,
+                    heads, page_size, table, batch, pages_per_seq, _ints(q_start, index, "q_start", batch + 1),
+                    _ints(kv_len, index, "kv_len", batch), most, int(window), int(sinks), _mask_bytes(sign_mask), softmax_scale, op,
+                    _DT[out.dtype], ws.data_ptr(), need)
     _check("tq3_attention_chunk", st)
     return out
 
