@@ -37,7 +37,7 @@
 namespace wq {
 namespace tq3_chunk_mma {  // tq3_chunk_mma.cu
 int64_t workspace();
-wq_status run(const tq3_chunk::Args &a, bool wide, cudaStream_t s);
+wq_status run(const tq3_chunk::Args &a, bool wide, const tq3_chunk::Args &few, int few_ctas, cudaStream_t s);
 unsigned int read_and_clear_fault();
 }  // namespace tq3_chunk_mma
 namespace tq3_chunk {
@@ -592,7 +592,6 @@ wq_status run_rows(const Args &a, cudaStream_t s) {
     using L = Layout<NT, kWide>;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(rows_kernel<NT, kWide>), L::kBytes)) return WQ_ERR_CUDA;
     launch_pdl(rows_kernel<NT, kWide>, kParts, kThreads, L::kBytes, s, a);
-    launch_join<L::kRows>(a, kParts, s);
     return launch_status();
 }
 
@@ -655,8 +654,13 @@ extern "C" wq_status tq3_attention_chunk(const void *q, int q_dtype, int64_t n_t
     const bool few = max_q <= tq3_chunk::kFewRows / group;
     if (!few) a.rows_to = tq3_chunk::kFewRows + 1;
     const wq_status st = wide ? tq3_chunk::run_rows<1, true>(a, s) : tq3_chunk::run_rows<1, false>(a, s);
-    if (few || st != WQ_OK) return st;
-    a.rows_from = a.rows_to, a.rows_to = INT32_MAX;
-    a.ws += tq3_chunk::rows_workspace();
-    return tq3_chunk_mma::run(a, wide, s);
+    if (st != WQ_OK) return st;
+    if (few) {
+        tq3_chunk::launch_join<8>(a, tq3_chunk::kParts, a, 0, s);
+        return launch_status();
+    }
+    tq3_chunk::Args many = a;
+    many.rows_from = a.rows_to, many.rows_to = INT32_MAX;
+    many.ws += tq3_chunk::rows_workspace();
+    return tq3_chunk_mma::run(many, wide, a, tq3_chunk::kParts, s);
 }

@@ -371,15 +371,14 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-// Joins the partial results of the segments that parts leave cut: CTA (x, y) rows y * kThreads / 32 on of
-// part x's, a warp a row.
-template <int R, int kThreads>
-__device__ __forceinline__ void merge_cut(const Args &a) {
-    const int part = blockIdx.x, ctas = gridDim.x, lane = threadIdx.x & 31;
+// Joins the partial results of the segment that part `part` leaves cut: its row r, by a warp.
+template <int R>
+__device__ __forceinline__ void merge_cut(const Args &a, int part, int ctas, int r) {
+    const int lane = threadIdx.x & 31;
     const Cut c = *reinterpret_cast<const Cut *>(a.ws + (int64_t)part * kCutBytes);
     if (!c.cut) return;
     const Seq s = load_seq(a, c.seq);
-    const int r = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5), row = c.block * R + r;
+    const int row = c.block * R + r;
     if (row >= s.new_tokens * a.group) return;
     const float *const slots = slot_at<R>(a, ctas, 2 * part);  // the part's own one is its second
     auto slot = [&](int i) { return slots + (i == 0 ? 1 : 2 * i) * slot_floats<R>(); };
@@ -414,24 +413,24 @@ __device__ __forceinline__ void merge_cut(const Args &a) {
     store_row<false>(a, s, c.head, row, lane, sg, v);
 }
 
-constexpr int kJoinThreads = 128;
-template <int R>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args a) {
+// The join of one launch, or of the two that share a call: `few` of R = 8 over few_ctas CTAs, then `many` of
+// RM rows over many_ctas.
+constexpr int kJoinThreads = 128, kJoinRows = kJoinThreads / 32;
+template <int RM>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Args few, int few_ctas,
+                                                            const __grid_constant__ Args many, int many_ctas) {
     pdl_wait();
-    merge_cut<R, kJoinThreads>(a);
+    constexpr int kFew = 8 / kJoinRows, kMany = RM / kJoinRows;
+    const int warp = threadIdx.x >> 5, i = blockIdx.x, j = i - few_ctas * kFew;
+    if (j < 0)
+        merge_cut<8>(few, i / kFew, few_ctas, i % kFew * kJoinRows + warp);
+    else
+        merge_cut<RM>(many, j / kMany, many_ctas, j % kMany * kJoinRows + warp);
 }
-template <int R>
-void launch_join(const Args &a, int ctas, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, R / (kJoinThreads / 32));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, join_kernel<R>, a);
+template <int RM>
+cudaError_t launch_join(const Args &few, int few_ctas, const Args &many, int many_ctas, cudaStream_t s) {
+    return launch_pdl(join_kernel<RM>, few_ctas * (8 / kJoinRows) + many_ctas * (RM / kJoinRows), kJoinThreads, 0, s, few,
+                      few_ctas, many, many_ctas);
 }
 
 }  // namespace tq3_chunk

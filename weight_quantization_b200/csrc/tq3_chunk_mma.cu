@@ -12,14 +12,14 @@
 // instead: a row that sees it gets NaN, any other is not touched.
 //
 // One CTA of 20 warps per SM. Warps 0-3 and 4-7 are the softmax of rows 0-127 and 128-255: a thread a row,
-// which lies in its tensor-memory lane. Warps 8-11 decode keys and 12-15 values: a thread a record. Warp 16
-// issues the products; 17-19 fill its warpgroup.
+// which lies in its tensor-memory lane. Warps 8-11 decode keys and 12-15 values: a thread a record. Warps 16
+// and 17 issue the products of a block each; 18 and 19 fill their warpgroup.
 //     decode   the eight centroids times the record's factor as a table of two bytes each; indices to the
 //              selectors of byte permutes, which fetch the bytes of four operands at a time; 16-byte
 //              chunks into the 128-byte-swizzled operand tile (K as K-major B, V as MN-major B)
 //     softmax  the maximum of a row of S; M is raised where it is passed by 2^8 (O is rescaled then);
 //              w = 2^(s - M), P as fp16 over S's columns that have been read
-//     issue    S0(0) S1(0) | P0(i) V(i) -> O0, S0(i+1) | P1(i) V(i) -> O1, S1(i+1) | ...
+//     issue    of a block: S(0) | P(0) V(0) -> O, S(1) | P(1) V(1) -> O, S(2) | ...
 // so that the tensor core works on one half of the rows while the other half's softmax runs. S(i+1) is
 // issued behind O(i), so a row whose S(i+1) has arrived may touch O. For fp32 queries or results the
 // operands are split hi + lo, a product takes three passes (hi hi, hi lo, lo hi), and 128 rows and one
@@ -89,7 +89,7 @@ struct Tile {          // of a stage
     uint32_t valid[4]; // keys that have a page
 };
 struct Shared {
-    uint64_t full_k[2], full_v[2], free_k[2], free_v[2], s_done[2], p_ready[2], o_done[2], q_ready, drain;
+    uint64_t full_k[2], full_v[2], free_k[2], free_v[2], s_done[2], p_ready[2], o_done[2], q_ready, drain[2];
     Tile tile[2];
     uint32_t tmem;
     float down;        // 2^-u
@@ -154,19 +154,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-// Waits for a phase for kWaitLimitNs at most. The clock is first read after some microseconds of polls:
-// reading it costs more than most of these waits last.
+// Waits for a phase for kWaitLimitNs at most. A poll may suspend the thread for up to kPollNs, so that
+// waiting warps leave the issue slots to the others; the clock, which is slow to read, only bounds waits
+// whose first polls have failed.
+constexpr uint32_t kPollNs = 100000;
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t phase) {
     const uint32_t at = smem_u32(bar);
     uint64_t t0 = 0;
+#pragma unroll 1
     for (uint32_t it = 0; it < kMaxPolls; ++it) {
         uint32_t ok;
-        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
                      : "=r"(ok)
-                     : "r"(at), "r"(phase)
+                     : "r"(at), "r"(phase), "r"(kPollNs)
                      : "memory");
         if (ok) return true;
-        if ((it & 255) == 255) {
+        if ((it & 63) == 63) {
             if (t0 == 0)
                 t0 = global_ns();
             else if (global_ns() - t0 > kWaitLimitNs)
@@ -257,6 +260,29 @@ __device__ __forceinline__ uint32_t visible(const Args &a, int pos, int j) {
     return m;
 }
 
+__device__ __forceinline__ float max32(float m, const float (&x)[32]) {
+    float n = x[0];
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) m = max3(m, x[k], x[k + 1]), n = max3(n, x[k + 2], x[k + 3]);
+    return fmaxf(m, n);
+}
+// w = 2^(s - M) of 32 columns of S, their sums, and P (hi, and lo behind it) to tensor memory.
+template <bool kWide>
+__device__ __forceinline__ void weights(const float (&x)[32], f32x2 M2, f32x2 (&ps)[2], uint32_t tP) {
+    uint32_t p[16], l[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        float d0, d1;
+        upk2(sub2(pk2(x[2 * k], x[2 * k + 1]), M2), d0, d1);
+        d0 = ex2(d0), d1 = ex2(d1);
+        ps[k & 1] = add2(ps[k & 1], pk2(d0, d1));
+        p[k] = h2(d0, d1);
+        if (kWide) l[k] = h2(__fsub_rn(d0, f2(p[k]).x), __fsub_rn(d1, f2(p[k]).y));
+    }
+    tmem_st16(tP, p);
+    if (kWide) tmem_st16(tP + 16, l);
+}
+
 // What every role knows of a segment.
 template <bool kWide>
 struct Segment {
@@ -301,7 +327,7 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
     const uint32_t tS = tmem + blk * 128 + lanes, tO = tmem + C::kTmemO + blk * 128 + lanes,
                    tP = tmem + C::kTmemP + blk * 128 + lanes;
     bool dead = false;
-    uint32_t n_tile = 0, n_s = 0, n_out = 0;  // tiles; of this warp's block: S products, results
+    uint32_t n_tile = 0, n_s = 0, n_out[2] = {};  // tiles; S products of this warp's block; results of each block
     float sg[4];
     lane_signs(a, lane, sg);
     while (!w.done()) {
@@ -394,18 +420,17 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
                     }
                     tmem_st_wait();
                 }
-                float mx = -INFINITY;
+                // S passes twice in pieces of 32 columns, each asked for while the one before is worked on
+                float x[32], y[32], mx = -INFINITY;
+                tmem_ld32(tS, x);
 #pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    float x[32], y[32];
-                    tmem_ld32(tS + 64 * c, x);
-                    tmem_ld32(tS + 64 * c + 32, y);
+                for (int c = 0; c < 128; c += 64) {
                     tmem_wait(x);
+                    tmem_ld32(tS + c + 32, y);
+                    mx = max32(mx, x);
                     tmem_wait(y);
-                    float m0 = x[0], m1 = y[0];
-#pragma unroll
-                    for (int k = 0; k < 32; k += 2) m0 = max3(m0, x[k], x[k + 1]), m1 = max3(m1, y[k], y[k + 1]);
-                    mx = max3(mx, m0, m1);
+                    tmem_ld32(tS + (c == 0 ? 64 : 0), x);
+                    mx = max32(mx, y);
                 }
                 float scale = t.ratio;  // of O, before this tile's product
                 G = t.G;
@@ -417,31 +442,19 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
                 }
                 const float Mo = __fsub_rn(M, kLift);
                 const f32x2 M2 = pk2(Mo, Mo);
-                f32x2 ps0 = pk2(0.0f, 0.0f), ps1 = ps0;
-                // P's 16 columns of a step lie over columns of S that have been read
+                f32x2 ps[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
+                // P's columns of a piece lie over columns of S that have been read twice
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    float x[32];
-                    tmem_ld32(tS + 32 * c, x);
+                for (int c = 0; c < 4; c += 2) {
                     tmem_wait(x);
-                    uint32_t p[16], l[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float d0, d1;
-                        upk2(sub2(pk2(x[2 * k], x[2 * k + 1]), M2), d0, d1);
-                        d0 = ex2(d0), d1 = ex2(d1);
-                        if (k & 1)
-                            ps1 = add2(ps1, pk2(d0, d1));
-                        else
-                            ps0 = add2(ps0, pk2(d0, d1));
-                        p[k] = h2(d0, d1);
-                        if (kWide) l[k] = h2(__fsub_rn(d0, f2(p[k]).x), __fsub_rn(d1, f2(p[k]).y));
-                    }
-                    tmem_st16(tP + (kWide ? 32 : 16) * c, p);
-                    if (kWide) tmem_st16(tP + 32 * c + 16, l);
+                    tmem_ld32(tS + 32 * c + 32, y);
+                    weights<kWide>(x, M2, ps, tP + (kWide ? 32 : 16) * c);
+                    tmem_wait(y);
+                    if (c == 0) tmem_ld32(tS + 64, x);
+                    weights<kWide>(y, M2, ps, tP + (kWide ? 32 : 16) * (c + 1));
                 }
                 float s0, s1;
-                upk2(add2(ps0, ps1), s0, s1);
+                upk2(add2(ps[0], ps[1]), s0, s1);
                 sum = __fadd_rn(sum, __fadd_rn(s0, s1));
                 if (i > 0 && __any_sync(0xffffffffu, scale != 1.0f)) {
 #pragma unroll 1
@@ -459,12 +472,14 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p_ready[blk]);
             }
-            if (!dead && !warp_wait(&sh.o_done[blk], n_out & 1u)) dead = true;
-            ++n_out;
+            // (both blocks': the results pass through the shared memory of both blocks' operands)
+            if (!dead && (!warp_wait(&sh.o_done[0], n_out[0] & 1u) || (g.nb == 2 && !warp_wait(&sh.o_done[1], n_out[1] & 1u))))
+                dead = true;
             tc_fence_after();
         }
+        if (!g.blind) ++n_out[0], n_out[1] += g.nb == 2;
         // the rows: finished, or a part of a cut segment. Their sums pass through shared memory (Q and K:
-        // every S product is done) from a thread a row to a warp a row
+        // every product is done) from a thread a row to a warp a row
         if (n_rows > 0 && !dead) {
             const float f = g.blind || sum == 0.0f ? 0.0f : __fmul_rn(__frcp_rn(sum), __fmul_rn(G, 1.0f / kVTop));
             unsigned char *const stage = base + C::kOffQ + warp * 16384;
@@ -653,7 +668,7 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Warp 16.
+// Warps 16 .. 15 + NB, one per block of rows.
 template <bool kWide>
 __device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned char *base, uint32_t tmem_) {
     using C = Cfg<kWide>;
@@ -661,68 +676,57 @@ __device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned c
     constexpr uint32_t kBlockOp = C::kParts * kOp >> 4, kLo = kOp >> 4;  // in units of a descriptor's address
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
     bool dead = false;
-    uint32_t n_tile = 0, segs = 0, n_s0 = 0, n_s1 = 0;  // n_s: S products of a block
+    uint32_t n_tile = 0, segs = 0, n_s = 0;  // n_s: S products of the block
+    const uint32_t blk = uniform(threadIdx.x / 32 - kIssueWarp);
     const uint32_t tmem = uniform(tmem_), at = uniform(smem_u32(base));
-    const uint32_t q0 = k_desc(at + C::kOffQ), k0 = k_desc(at + C::kOffK), v0 = mn_desc(at + C::kOffV);
+    const uint32_t q = k_desc(at + C::kOffQ) + blk * kBlockOp, k0 = k_desc(at + C::kOffK), v0 = mn_desc(at + C::kOffV);
+    const uint32_t tS = tmem + blk * 128, tO = tmem + C::kTmemO + blk * 128, tP = tmem + C::kTmemP + blk * 128;
     while (!w.done()) {
         const Segment<kWide> g(a, w);
-        const uint32_t take = uniform(g.blind ? 0 : g.take), nb = uniform(g.nb);
-        if (take > 0 && !dead && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
+        const uint32_t take = uniform(g.blind ? 0 : g.take), nb = uniform(g.nb), mine = blk < nb ? take : 0;
+        if (mine > 0 && !dead && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
 #pragma unroll 1
-        for (uint32_t i = 0; i <= take && take > 0 && !dead; ++i) {
+        for (uint32_t i = 0; i <= mine && mine > 0 && !dead; ++i) {
             const uint32_t n = n_tile + i, st = n % KS, before = (n - 1) % KS;
-#pragma unroll 1
-            for (uint32_t blk = 0; blk < nb; ++blk) {
+            if ((i < mine && !warp_wait(&sh.full_k[st], (n / KS) & 1u)) ||
+                (i > 0 && (!warp_wait(&sh.full_v[before], ((n - 1) / KS) & 1u) || !warp_wait(&sh.p_ready[blk], (n_s - 1) & 1u)))) {
+                dead = true;
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
                 if (i > 0) {  // O of tile i - 1
-                    if ((blk == 0 && !warp_wait(&sh.full_v[before], ((n - 1) / KS) & 1u)) ||
-                        !warp_wait(&sh.p_ready[blk], ((blk ? n_s1 : n_s0) - 1) & 1u)) {
-                        dead = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t d = tmem + C::kTmemO + blk * 128, p0 = tmem + C::kTmemP + blk * 128;
 #pragma unroll
-                        for (int ps = 0; ps < kPasses; ++ps) {
-                            const uint32_t v = v0 + before * kBlockOp + (ps == 1 ? kLo : 0);
+                    for (int ps = 0; ps < kPasses; ++ps) {
+                        const uint32_t v = v0 + before * kBlockOp + (ps == 1 ? kLo : 0);
 #pragma unroll
-                            for (int ks = 0; ks < 8; ++ks)
-                                mma_ts(d, p0 + (kWide ? 32 * (ks >> 1) + 8 * (ks & 1) + (ps == 2 ? 16 : 0) : 8 * ks),
-                                       v + ks * (2048 >> 4), kIdescO, i > 1 || ps > 0 || ks > 0);
-                        }
-                        if (blk == nb - 1) mma_commit(&sh.free_v[before]);
-                        if (i == take) mma_commit(&sh.o_done[blk]);
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_ts(tO, tP + (kWide ? 32 * (ks >> 1) + 8 * (ks & 1) + (ps == 2 ? 16 : 0) : 8 * ks),
+                                   v + ks * (2048 >> 4), kIdescO, i > 1 || ps > 0 || ks > 0);
                     }
-                    __syncwarp();
+                    mma_commit(&sh.free_v[before]);
+                    if (i == mine) mma_commit(&sh.o_done[blk]);
                 }
-                if (i < take) {
-                    if (blk == 0) {
-                        if (!warp_wait(&sh.full_k[st], (n / KS) & 1u)) {
-                            dead = true;
-                            break;
-                        }
-                        tc_fence_after();
-                    }
-                    if (elect_one()) {
+                if (i < mine) {
 #pragma unroll
-                        for (int ps = 0; ps < kPasses; ++ps) {
-                            const uint32_t q = q0 + blk * kBlockOp + (ps == 2 ? kLo : 0), k = k0 + st * kBlockOp + (ps == 1 ? kLo : 0);
+                    for (int ps = 0; ps < kPasses; ++ps) {
+                        const uint32_t qa = q + (ps == 2 ? kLo : 0), k = k0 + st * kBlockOp + (ps == 1 ? kLo : 0);
 #pragma unroll
-                            for (int ks = 0; ks < 8; ++ks) {
-                                const uint32_t off = (uint32_t)((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
-                                mma_ss(tmem + blk * 128, q + off, k + off, kIdescS, ps > 0 || ks > 0);
-                            }
+                        for (int ks = 0; ks < 8; ++ks) {
+                            const uint32_t off = (uint32_t)((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
+                            mma_ss(tS, qa + off, k + off, kIdescS, ps > 0 || ks > 0);
                         }
-                        mma_commit(&sh.s_done[blk]);
-                        if (blk == nb - 1) mma_commit(&sh.free_k[st]);
                     }
-                    __syncwarp();
-                    if (blk)
-                        ++n_s1;
-                    else
-                        ++n_s0;
+                    mma_commit(&sh.s_done[blk]);
+                    mma_commit(&sh.free_k[st]);
+                }
+                if (nb < C::NB) {  // a block without rows frees its share
+                    if (i > 0) mbar_arrive(&sh.free_v[before]);
+                    if (i < mine) mbar_arrive(&sh.free_k[st]);
                 }
             }
+            __syncwarp();
+            n_s += i < mine;
         }
         ++segs;
         n_tile += take;
@@ -744,17 +748,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.full_k[i], 4);
             mbar_init(&sh.full_v[i], 4);
-            mbar_init(&sh.free_k[i], 1);
-            mbar_init(&sh.free_v[i], 1);
+            mbar_init(&sh.free_k[i], NB);
+            mbar_init(&sh.free_v[i], NB);
             mbar_init(&sh.s_done[i], 1);
             mbar_init(&sh.p_ready[i], 4);
             mbar_init(&sh.o_done[i], 1);
         }
         mbar_init(&sh.q_ready, 4 * NB);
-        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.drain[0], 1);
+        mbar_init(&sh.drain[1], 1);
     }
     if (warp == kIssueWarp) tmem_alloc(&sh.tmem, 512);
-    pdl_wait();
+    // No wait here: the rows kernel, launched before this one in the same call, lets it start only when all
+    // that this call reads has been written, and the two share nothing that either writes.
     Cut *const cut = reinterpret_cast<Cut *>(a.ws + (int64_t)blockIdx.x * kCutBytes);
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
     {
@@ -785,16 +791,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         dead = decode_role<kWide>(a, sh, base);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-        if (warp == kIssueWarp)
+        if (warp < kIssueWarp + NB)
             dead = issue_role<kWide>(a, sh, base, tmem);
         else
             while (!w.done()) next_segment<kWide>(a, w, false);
     }
     pdl_trigger();
+    pdl_wait();  // the join behind this kernel also needs the rows kernel's results
     // products still in flight after a wait ran out get a bounded chance to finish
-    if (warp == kIssueWarp && dead && lane == 0) {
-        mma_commit(&sh.drain);
-        mbar_wait_bounded(&sh.drain, 0, kMaxPolls);
+    if (warp >= kIssueWarp && dead && lane == 0) {
+        mma_commit(&sh.drain[warp - kIssueWarp]);
+        mbar_wait_bounded(&sh.drain[warp - kIssueWarp], 0, kMaxPolls);
     }
     tc_fence_before();
     __syncthreads();
@@ -813,15 +820,18 @@ unsigned int read_and_clear_fault() {
 
 int64_t workspace() { return tq3_chunk::workspace_bytes<256>(kSms); }
 
+// Follows the rows kernel of the same call, whose results and own ones it leaves to one join.
 template <bool kWide>
-wq_status run(const Args &a, cudaStream_t s) {
+wq_status run(const Args &a, const Args &few, int few_ctas, cudaStream_t s) {
     using C = Cfg<kWide>;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(chunk_kernel<kWide>), C::kSmem)) return WQ_ERR_CUDA;
     launch_pdl(chunk_kernel<kWide>, kSms, kThreads, C::kSmem, s, a);
-    launch_join<C::R>(a, kSms, s);
+    launch_join<C::R>(few, few_ctas, a, kSms, s);
     return launch_status();
 }
-wq_status run(const Args &a, bool wide, cudaStream_t s) { return wide ? run<true>(a, s) : run<false>(a, s); }
+wq_status run(const Args &a, bool wide, const Args &few, int few_ctas, cudaStream_t s) {
+    return wide ? run<true>(a, few, few_ctas, s) : run<false>(a, few, few_ctas, s);
+}
 
 }  // namespace tq3_chunk_mma
 }  // namespace wq
