@@ -19,9 +19,11 @@
 //              chunks into the 128-byte-swizzled operand tile (K as K-major B, V as MN-major B)
 //     softmax  the maximum of a row of S; M is raised where it is passed by 2^8 (O is rescaled then);
 //              w = 2^(s - M), P as fp16 over S's columns that have been read
-//     issue    of a block: S(0) | P(0) V(0) -> O, S(1) | P(1) V(1) -> O, S(2) | ...
-// so that the tensor core works on one half of the rows while the other half's softmax runs. S(i+1) is
-// issued behind O(i), so a row whose S(i+1) has arrived may touch O. For fp32 queries or results the
+//     issue    of a block, with a and b the two 64-key halves of a tile:
+//              S(0a) S(0b) | P(0a) V(0a) -> O, S(1a) | P(0b) V(0b) -> O, S(1b) | ...
+// so that the softmax of one half runs while the tensor core works on the other, and the two blocks of rows
+// share it. Products run in the order of their issue: S(i+1 a) may overwrite P(i a), which lies over S(i a).
+// For fp32 queries or results the
 // operands are split hi + lo, a product takes three passes (hi hi, hi lo, lo hi), and 128 rows and one
 // stage of operands fill the shared memory.
 //
@@ -60,9 +62,9 @@ constexpr int kRecStages = 2;
 constexpr int kQBits = 7;             // a bound of |q~| of a segment is scaled to 2^7 .. 2^8
 constexpr float kVTop = 8192.0f;      // a value of factor G has this one
 
-// fp16 operands, fp32 accumulator, M = N = 128; B of the value product is MN-major.
-constexpr uint32_t kIdescS = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr uint32_t kIdescO = kIdescS | (1u << 16);
+// fp16 operands, fp32 accumulator, M = 128; N = 64 keys, and N = 128 coordinates with an MN-major B.
+constexpr uint32_t kIdescS = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 
 __device__ unsigned int g_fault;
 
@@ -89,7 +91,8 @@ struct Tile {          // of a stage
     uint32_t valid[4]; // keys that have a page
 };
 struct Shared {
-    uint64_t full_k[2], full_v[2], free_k[2], free_v[2], s_done[2], p_ready[2], o_done[2], q_ready, drain[2];
+    uint64_t full_k[2], full_v[2], free_k[2], free_v[2], q_ready, drain[2];
+    uint64_t s_done[2][2], p_ready[2][2], pv_done[2], o_done[2];  // per block (and half of a tile)
     Tile tile[2];
     uint32_t tmem;
     float down;        // 2^-u
@@ -327,7 +330,7 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
     const uint32_t tS = tmem + blk * 128 + lanes, tO = tmem + C::kTmemO + blk * 128 + lanes,
                    tP = tmem + C::kTmemP + blk * 128 + lanes;
     bool dead = false;
-    uint32_t n_tile = 0, n_s = 0, n_out[2] = {};  // tiles; S products of this warp's block; results of each block
+    uint32_t n_tile = 0, n_s = 0, n_out[2] = {};  // tiles; tiles of this warp's block; results of each block
     float sg[4];
     lane_signs(a, lane, sg);
     while (!w.done()) {
@@ -394,46 +397,35 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
             // positions of the warp's rows, for tiles that all of them see whole
             const int lo = g.before + token_of(a, min(wr, g.rows - 1)), hi = g.before + token_of(a, min(wr + 31, g.rows - 1));
 #pragma unroll 1
-            for (int i = 0; i < g.take; ++i) {
+            for (int step = 0; step < 2 * g.take; ++step) {  // halves of a tile
+                const int i = step >> 1, half = step & 1;
                 const uint32_t n = n_tile + i, st = n % KS;
-                const int j0 = g.span.tile(g.first + i) * kTileKeys;
-                if (!warp_wait(&sh.full_v[st], (n / KS) & 1u) || !warp_wait(&sh.s_done[blk], n_s & 1u)) {
+                const int j0 = g.span.tile(g.first + i) * kTileKeys + 64 * half;
+                if ((half == 0 && !warp_wait(&sh.full_v[st], (n / KS) & 1u)) || !warp_wait(&sh.s_done[blk][half], n_s & 1u)) {
                     dead = true;
                     break;
                 }
-                ++n_s;
                 tc_fence_after();
                 const Tile &t = sh.tile[st];
-                const bool full = (t.valid[0] & t.valid[1] & t.valid[2] & t.valid[3]) == 0xffffffffu &&
-                                  j0 + kTileKeys <= lo + 1 &&
-                                  (a.window == 0 || j0 > hi - a.window || j0 + kTileKeys <= a.sinks);
-                if (!full) {  // -inf where the row does not see the key
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float x[32];
-                        tmem_ld32(tS + 32 * c, x);
-                        tmem_wait(x);
-                        const uint32_t on = visible(a, pos, j0 + 32 * c) & t.valid[c];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = (on >> k & 1u) ? x[k] : -INFINITY;
-                        tmem_st32(tS + 32 * c, x);
-                    }
-                    tmem_st_wait();
-                }
-                // S passes twice in pieces of 32 columns, each asked for while the one before is worked on
-                float x[32], y[32], mx = -INFINITY;
-                tmem_ld32(tS, x);
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 64) {
-                    tmem_wait(x);
-                    tmem_ld32(tS + c + 32, y);
-                    mx = max32(mx, x);
-                    tmem_wait(y);
-                    tmem_ld32(tS + (c == 0 ? 64 : 0), x);
-                    mx = max32(mx, y);
-                }
-                float scale = t.ratio;  // of O, before this tile's product
+                float x[32], y[32];
+                tmem_ld32(tS + 64 * half, x);
+                tmem_ld32(tS + 64 * half + 32, y);
+                const uint32_t v0 = t.valid[2 * half], v1 = t.valid[2 * half + 1];
+                float scale = half ? 1.0f : t.ratio;  // of O, before this half's product
                 G = t.G;
+                const bool full = (v0 & v1) == 0xffffffffu && j0 + 64 <= lo + 1 &&
+                                  (a.window == 0 || j0 > hi - a.window || j0 + 64 <= a.sinks);
+                tmem_wait(x);
+                tmem_wait(y);
+                if (!full) {  // -inf where the row does not see the key
+                    const uint32_t on0 = visible(a, pos, j0) & v0, on1 = visible(a, pos, j0 + 32) & v1;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        x[k] = (on0 >> k & 1u) ? x[k] : -INFINITY;
+                        y[k] = (on1 >> k & 1u) ? y[k] : -INFINITY;
+                    }
+                }
+                const float mx = max32(max32(-INFINITY, x), y);
                 if (__any_sync(0xffffffffu, mx > __fadd_rn(M, kLazy))) {  // every row of the warp takes its own maximum
                     const float m = fmaxf(M, mx), alpha = ex2(__fsub_rn(M, m));
                     M = m;
@@ -443,34 +435,33 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
                 const float Mo = __fsub_rn(M, kLift);
                 const f32x2 M2 = pk2(Mo, Mo);
                 f32x2 ps[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
-                // P's columns of a piece lie over columns of S that have been read twice
-#pragma unroll 1
-                for (int c = 0; c < 4; c += 2) {
-                    tmem_wait(x);
-                    tmem_ld32(tS + 32 * c + 32, y);
-                    weights<kWide>(x, M2, ps, tP + (kWide ? 32 : 16) * c);
-                    tmem_wait(y);
-                    if (c == 0) tmem_ld32(tS + 64, x);
-                    weights<kWide>(y, M2, ps, tP + (kWide ? 32 : 16) * (c + 1));
-                }
+                // P's columns lie over the half's columns of S
+                weights<kWide>(x, M2, ps, tP + 64 * half);
+                weights<kWide>(y, M2, ps, tP + 64 * half + (kWide ? 32 : 16));
                 float s0, s1;
                 upk2(add2(ps[0], ps[1]), s0, s1);
                 sum = __fadd_rn(sum, __fadd_rn(s0, s1));
-                if (i > 0 && __any_sync(0xffffffffu, scale != 1.0f)) {
+                if (step > 0 && __any_sync(0xffffffffu, scale != 1.0f)) {
+                    // the product of the half before has to be in O first
+                    if (!warp_wait(&sh.pv_done[blk], (2 * n_s + half - 1) & 1u)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        float o[32];
-                        tmem_ld32(tO + 32 * c, o);
-                        tmem_wait(o);
+                        tmem_ld32(tO + 32 * c, x);
+                        tmem_wait(x);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __fmul_rn(o[k], scale);
-                        tmem_st32(tO + 32 * c, o);
+                        for (int k = 0; k < 32; ++k) x[k] = __fmul_rn(x[k], scale);
+                        tmem_st32(tO + 32 * c, x);
                     }
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready[blk]);
+                if (lane == 0) mbar_arrive(&sh.p_ready[blk][half]);
+                n_s += half;
             }
             // (both blocks': the results pass through the shared memory of both blocks' operands)
             if (!dead && (!warp_wait(&sh.o_done[0], n_out[0] & 1u) || (g.nb == 2 && !warp_wait(&sh.o_done[1], n_out[1] & 1u))))
@@ -673,10 +664,10 @@ template <bool kWide>
 __device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned char *base, uint32_t tmem_) {
     using C = Cfg<kWide>;
     constexpr int KS = C::KS, R = C::R, kPasses = kWide ? 3 : 1;
-    constexpr uint32_t kBlockOp = C::kParts * kOp >> 4, kLo = kOp >> 4;  // in units of a descriptor's address
+    constexpr uint32_t kBlockOp = C::kParts * kOp >> 4, kLo = kOp >> 4, kHalf = 64 * 128 >> 4;  // in units of a descriptor's address
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
     bool dead = false;
-    uint32_t n_tile = 0, segs = 0, n_s = 0;  // n_s: S products of the block
+    uint32_t n_tile = 0, segs = 0, n_s = 0;  // n_s: tiles of the block
     const uint32_t blk = uniform(threadIdx.x / 32 - kIssueWarp);
     const uint32_t tmem = uniform(tmem_), at = uniform(smem_u32(base));
     const uint32_t q = k_desc(at + C::kOffQ) + blk * kBlockOp, k0 = k_desc(at + C::kOffK), v0 = mn_desc(at + C::kOffV);
@@ -686,48 +677,51 @@ __device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned c
         const uint32_t take = uniform(g.blind ? 0 : g.take), nb = uniform(g.nb), mine = blk < nb ? take : 0;
         if (mine > 0 && !dead && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
 #pragma unroll 1
-        for (uint32_t i = 0; i <= mine && mine > 0 && !dead; ++i) {
-            const uint32_t n = n_tile + i, st = n % KS, before = (n - 1) % KS;
-            if ((i < mine && !warp_wait(&sh.full_k[st], (n / KS) & 1u)) ||
-                (i > 0 && (!warp_wait(&sh.full_v[before], ((n - 1) / KS) & 1u) || !warp_wait(&sh.p_ready[blk], (n_s - 1) & 1u)))) {
+        for (uint32_t step = 0; step < 2 * mine + 2 && mine > 0 && !dead; ++step) {
+            // S of half `half` of tile i, behind the value product of that half of tile i - 1
+            const uint32_t i = step >> 1, half = step & 1, n = n_tile + i, st = n % KS, before = (n - 1) % KS;
+            if ((i < mine && half == 0 && !warp_wait(&sh.full_k[st], (n / KS) & 1u)) ||
+                (i > 0 && ((half == 0 && !warp_wait(&sh.full_v[before], ((n - 1) / KS) & 1u)) ||
+                           !warp_wait(&sh.p_ready[blk][half], (n_s + i - 1) & 1u)))) {
                 dead = true;
                 break;
             }
             tc_fence_after();
             if (elect_one()) {
-                if (i > 0) {  // O of tile i - 1
+                if (i > 0) {
 #pragma unroll
                     for (int ps = 0; ps < kPasses; ++ps) {
-                        const uint32_t v = v0 + before * kBlockOp + (ps == 1 ? kLo : 0);
+                        const uint32_t v = v0 + before * kBlockOp + half * kHalf + (ps == 1 ? kLo : 0);
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_ts(tO, tP + (kWide ? 32 * (ks >> 1) + 8 * (ks & 1) + (ps == 2 ? 16 : 0) : 8 * ks),
-                                   v + ks * (2048 >> 4), kIdescO, i > 1 || ps > 0 || ks > 0);
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ts(tO, tP + 64 * half + (kWide ? 32 * (ks >> 1) + 8 * (ks & 1) + (ps == 2 ? 16 : 0) : 8 * ks),
+                                   v + ks * (2048 >> 4), kIdescO, step > 2 || ps > 0 || ks > 0);
                     }
-                    mma_commit(&sh.free_v[before]);
-                    if (i == mine) mma_commit(&sh.o_done[blk]);
+                    mma_commit(&sh.pv_done[blk]);
+                    if (half) mma_commit(&sh.free_v[before]);
+                    if (step == 2 * mine + 1) mma_commit(&sh.o_done[blk]);
                 }
                 if (i < mine) {
 #pragma unroll
                     for (int ps = 0; ps < kPasses; ++ps) {
-                        const uint32_t qa = q + (ps == 2 ? kLo : 0), k = k0 + st * kBlockOp + (ps == 1 ? kLo : 0);
+                        const uint32_t qa = q + (ps == 2 ? kLo : 0), k = k0 + st * kBlockOp + half * kHalf + (ps == 1 ? kLo : 0);
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks) {
                             const uint32_t off = (uint32_t)((ks >> 2) * kBox + (ks & 3) * 32) >> 4;
-                            mma_ss(tS, qa + off, k + off, kIdescS, ps > 0 || ks > 0);
+                            mma_ss(tS + 64 * half, qa + off, k + off, kIdescS, ps > 0 || ks > 0);
                         }
                     }
-                    mma_commit(&sh.s_done[blk]);
-                    mma_commit(&sh.free_k[st]);
+                    mma_commit(&sh.s_done[blk][half]);
+                    if (half) mma_commit(&sh.free_k[st]);
                 }
-                if (nb < C::NB) {  // a block without rows frees its share
+                if (nb < C::NB && half) {  // a block without rows frees its share
                     if (i > 0) mbar_arrive(&sh.free_v[before]);
                     if (i < mine) mbar_arrive(&sh.free_k[st]);
                 }
             }
             __syncwarp();
-            n_s += i < mine;
         }
+        n_s += mine;
         ++segs;
         n_tile += take;
         next_segment<kWide>(a, w, false);
@@ -750,8 +744,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(&sh.full_v[i], 4);
             mbar_init(&sh.free_k[i], NB);
             mbar_init(&sh.free_v[i], NB);
-            mbar_init(&sh.s_done[i], 1);
-            mbar_init(&sh.p_ready[i], 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&sh.s_done[i][h], 1);
+                mbar_init(&sh.p_ready[i][h], 4);
+            }
+            mbar_init(&sh.pv_done[i], 1);
             mbar_init(&sh.o_done[i], 1);
         }
         mbar_init(&sh.q_ready, 4 * NB);
