@@ -396,72 +396,78 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
             const int pos = lane < n_rows ? g.before + token_of(a, wr + lane) : -1;
             // positions of the warp's rows, for tiles that all of them see whole
             const int lo = g.before + token_of(a, min(wr, g.rows - 1)), hi = g.before + token_of(a, min(wr + 31, g.rows - 1));
+            float x[32], y[32];
 #pragma unroll 1
-            for (int step = 0; step < 2 * g.take; ++step) {  // halves of a tile
-                const int i = step >> 1, half = step & 1;
-                const uint32_t n = n_tile + i, st = n % KS;
-                const int j0 = g.span.tile(g.first + i) * kTileKeys + 64 * half;
-                if ((half == 0 && !warp_wait(&sh.full_v[st], (n / KS) & 1u)) || !warp_wait(&sh.s_done[blk][half], n_s & 1u)) {
+            for (int i = 0; i < g.take && !dead; ++i) {
+                const uint32_t st = (n_tile + i) % KS;
+                const int j0 = g.span.tile(g.first + i) * kTileKeys;
+                if (!warp_wait(&sh.full_v[st], ((n_tile + i) / KS) & 1u)) {
                     dead = true;
                     break;
                 }
-                tc_fence_after();
-                const Tile &t = sh.tile[st];
-                float x[32], y[32];
-                tmem_ld32(tS + 64 * half, x);
-                tmem_ld32(tS + 64 * half + 32, y);
-                const uint32_t v0 = t.valid[2 * half], v1 = t.valid[2 * half + 1];
-                float scale = half ? 1.0f : t.ratio;  // of O, before this half's product
+                const Tile t = sh.tile[st];
                 G = t.G;
-                const bool full = (v0 & v1) == 0xffffffffu && j0 + 64 <= lo + 1 &&
-                                  (a.window == 0 || j0 > hi - a.window || j0 + 64 <= a.sinks);
-                tmem_wait(x);
-                tmem_wait(y);
-                if (!full) {  // -inf where the row does not see the key
-                    const uint32_t on0 = visible(a, pos, j0) & v0, on1 = visible(a, pos, j0 + 32) & v1;
+                const bool full = (t.valid[0] & t.valid[1] & t.valid[2] & t.valid[3]) == 0xffffffffu && j0 + kTileKeys <= lo + 1 &&
+                                  (a.window == 0 || j0 > hi - a.window || j0 + kTileKeys <= a.sinks);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        x[k] = (on0 >> k & 1u) ? x[k] : -INFINITY;
-                        y[k] = (on1 >> k & 1u) ? y[k] : -INFINITY;
-                    }
-                }
-                const float mx = max32(max32(-INFINITY, x), y);
-                if (__any_sync(0xffffffffu, mx > __fadd_rn(M, kLazy))) {  // every row of the warp takes its own maximum
-                    const float m = fmaxf(M, mx), alpha = ex2(__fsub_rn(M, m));
-                    M = m;
-                    sum = __fmul_rn(sum, alpha);
-                    scale = __fmul_rn(scale, alpha);
-                }
-                const float Mo = __fsub_rn(M, kLift);
-                const f32x2 M2 = pk2(Mo, Mo);
-                f32x2 ps[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
-                // P's columns lie over the half's columns of S
-                weights<kWide>(x, M2, ps, tP + 64 * half);
-                weights<kWide>(y, M2, ps, tP + 64 * half + (kWide ? 32 : 16));
-                float s0, s1;
-                upk2(add2(ps[0], ps[1]), s0, s1);
-                sum = __fadd_rn(sum, __fadd_rn(s0, s1));
-                if (step > 0 && __any_sync(0xffffffffu, scale != 1.0f)) {
-                    // the product of the half before has to be in O first
-                    if (!warp_wait(&sh.pv_done[blk], (2 * n_s + half - 1) & 1u)) {
+                for (int half = 0; half < 2; ++half) {
+                    if (!warp_wait(&sh.s_done[blk][half], n_s & 1u)) {
                         dead = true;
                         break;
                     }
                     tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_ld32(tO + 32 * c, x);
-                        tmem_wait(x);
+                    tmem_ld32(tS + 64 * half, x);
+                    tmem_ld32(tS + 64 * half + 32, y);
+                    float scale = half ? 1.0f : t.ratio;  // of O, before this half's product
+                    tmem_wait(x);
+                    tmem_wait(y);
+                    if (!full) {  // -inf where the row does not see the key
+                        const uint32_t on0 = visible(a, pos, j0 + 64 * half) & t.valid[2 * half],
+                                       on1 = visible(a, pos, j0 + 64 * half + 32) & t.valid[2 * half + 1];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = __fmul_rn(x[k], scale);
-                        tmem_st32(tO + 32 * c, x);
+                        for (int k = 0; k < 32; ++k) {
+                            x[k] = (on0 >> k & 1u) ? x[k] : -INFINITY;
+                            y[k] = (on1 >> k & 1u) ? y[k] : -INFINITY;
+                        }
                     }
+                    const float mx = max32(max32(-INFINITY, x), y);
+                    if (__any_sync(0xffffffffu, mx > __fadd_rn(M, kLazy))) {  // every row of the warp takes its own maximum
+                        const float m = fmaxf(M, mx), alpha = ex2(__fsub_rn(M, m));
+                        M = m;
+                        sum = __fmul_rn(sum, alpha);
+                        scale = __fmul_rn(scale, alpha);
+                    }
+                    const float Mo = __fsub_rn(M, kLift);
+                    const f32x2 M2 = pk2(Mo, Mo);
+                    f32x2 ps[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
+                    // P's columns lie over the half's columns of S
+                    weights<kWide>(x, M2, ps, tP + 64 * half);
+                    weights<kWide>(y, M2, ps, tP + 64 * half + (kWide ? 32 : 16));
+                    float s0, s1;
+                    upk2(add2(ps[0], ps[1]), s0, s1);
+                    sum = __fadd_rn(sum, __fadd_rn(s0, s1));
+                    if ((half || i > 0) && __any_sync(0xffffffffu, scale != 1.0f)) {
+                        // the product of the half before has to be in O first
+                        if (!warp_wait(&sh.pv_done[blk], (half - 1) & 1u)) {
+                            dead = true;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_ld32(tO + 32 * c, x);
+                            tmem_wait(x);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[k] = __fmul_rn(x[k], scale);
+                            tmem_st32(tO + 32 * c, x);
+                        }
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_ready[blk][half]);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready[blk][half]);
-                n_s += half;
+                ++n_s;
             }
             // (both blocks': the results pass through the shared memory of both blocks' operands)
             if (!dead && (!warp_wait(&sh.o_done[0], n_out[0] & 1u) || (g.nb == 2 && !warp_wait(&sh.o_done[1], n_out[1] & 1u))))
