@@ -3,11 +3,11 @@
 // segment has NB x 128 rows and a tile of 128 keys is two products per 128 rows:
 //     S = Q~ K^T       (128 rows x 128 keys, K = 128 rotated coordinates; both operands in shared memory)
 //     O += P V         (128 rows x 128 coordinates, K = 128 keys; P in tensor memory, V in shared memory)
-// with K's row j = c[idx_j] f_j coef 2^-u and V's row j = c[idx'_j] g_j 2^13 / G in fp16. 2^u brings a
-// bound of the segment's |q~| to 2^7 .. 2^8, so that S is the logit in log2 units as it leaves the tensor
-// core and the softmax has no per-key factor to apply. What underflows in K then moves a logit by less
-// than 2^-13, and only the absolute error of a logit matters. G follows the largest g_j of the tiles so
-// far and is raised when one is passed by 4 (O is rescaled then), so a value keeps all its bits down to
+// with K's row j = c[idx_j] f_j coef 2^4 / F and V's row j = c[idx'_j] g_j 2^13 / G in fp16, F the power of
+// two at the tile's largest f_j coef, and each row of q~ scaled by a power of two to 2^7 .. 2^8: one factor per
+// row and tile leads from S to the logit in log2 units, and it rides on the subtraction of the maximum. What
+// underflows in K then moves a logit by less than 2^-20 of the tile's largest. G follows the largest g_j of the
+// tiles so far and is raised when one is passed by 4 (O is rescaled then), so a value keeps all its bits down to
 // 2^-27 of the largest. A value whose factor is not finite becomes zero and poisons its key's logits
 // instead: a row that sees it gets NaN, any other is not touched.
 //
@@ -23,9 +23,8 @@
 //              S(0a) S(0b) | P(0a) V(0a) -> O, S(1a) | P(0b) V(0b) -> O, S(1b) | ...
 // so that the softmax of one half runs while the tensor core works on the other, and the two blocks of rows
 // share it. Products run in the order of their issue: S(i+1 a) may overwrite P(i a), which lies over S(i a).
-// For fp32 queries or results the
-// operands are split hi + lo, a product takes three passes (hi hi, hi lo, lo hi), and 128 rows and one
-// stage of operands fill the shared memory.
+// For fp32 queries or results the operands are split hi + lo, a product takes three passes (hi hi, hi lo,
+// lo hi), and 128 rows and one stage of operands fill the shared memory.
 //
 // Every wait is bounded; one that runs out sets fault bit 7, ends its role, and the others run out after
 // it. In-flight products get a bounded chance to finish before the tensor memory is freed.
@@ -59,7 +58,8 @@ constexpr uint32_t kMaxPolls = 1u << 24;
 constexpr float kLazy = 8.0f, kLift = 6.0f;  // as in tq3_chunk.cu
 constexpr int kRecBytes = kTileKeys * tq3_cache::kRec;  // a tile's records of one pool
 constexpr int kRecStages = 2;
-constexpr int kQBits = 7;             // a bound of |q~| of a segment is scaled to 2^7 .. 2^8
+constexpr int kQBits = 7;             // the largest |q~| of a row is scaled to 2^7 .. 2^8
+constexpr float kKTop = 16.0f;        // a key of a factor that is the largest power of two in the tile has this one
 constexpr float kVTop = 8192.0f;      // a value of factor G has this one
 
 // fp16 operands, fp32 accumulator, M = 128; N = 64 keys, and N = 128 coordinates with an MN-major B.
@@ -94,10 +94,11 @@ struct Shared {
     uint64_t full_k[2], full_v[2], free_k[2], free_v[2], q_ready, drain[2];
     uint64_t s_done[2][2], p_ready[2][2], pv_done[2], o_done[2];  // per block (and half of a tile)
     Tile tile[2];
+    // what a unit of K stands for, of the last four tiles: keys are decoded up to KS tiles ahead of the one
+    // whose S is complete, and a softmax warp may be a tile behind that
+    float unit[4];
     uint32_t tmem;
-    float down;        // 2^-u
-    float top[8];      // per softmax warp: the largest sum of |q|
-    uint32_t gmax[2][4];
+    uint32_t most[2][2][4];  // per tile (alternately), pool and decoding warp: the largest factor
     int64_t scratch[kThreads / 32 + 4];
     Walk<256, kThreads> walk256;
     Walk<128, kThreads> walk128;
@@ -234,12 +235,13 @@ __device__ __forceinline__ void expand(unsigned char *op, int row, const uint32_
 #pragma unroll 1
     for (int part = 0; part < 4; ++part) {
         const uint32_t w0 = rec[3 * part], w1 = rec[3 * part + 1], w2 = rec[3 * part + 2];
-        unsigned char *const to = op + (part >> 1) * kBox + row * 128;
+        // chunk (4 (part & 1) + c) ^ (row & 7), its two low bits apart
+        unsigned char *const to = op + (part >> 1) * kBox + row * 128 + (((part & 1) << 6) ^ ((row & 4) << 4));
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const uint32_t x = c == 0 ? w0 : c == 1 ? __funnelshift_r(w0, w1, 24) : c == 2 ? __funnelshift_r(w1, w2, 16) : w2 >> 8;
             const uint32_t sel = nibbles(x);
-            unsigned char *const chunk = to + (((4 * (part & 1) + c) ^ (row & 7)) << 4);
+            unsigned char *const chunk = to + ((c ^ (row & 3)) << 4);
             uint4 h;
             four(th, sel, h.x, h.y);
             four(th, sel >> 16, h.z, h.w);
@@ -269,14 +271,14 @@ __device__ __forceinline__ float max32(float m, const float (&x)[32]) {
     for (int k = 0; k < 32; k += 4) m = max3(m, x[k], x[k + 1]), n = max3(n, x[k + 2], x[k + 3]);
     return fmaxf(m, n);
 }
-// w = 2^(s - M) of 32 columns of S, their sums, and P (hi, and lo behind it) to tensor memory.
+// w = 2^(S U - M) of 32 columns of S, their sums, and P (hi, and lo behind it) to tensor memory.
 template <bool kWide>
-__device__ __forceinline__ void weights(const float (&x)[32], f32x2 M2, f32x2 (&ps)[2], uint32_t tP) {
+__device__ __forceinline__ void weights(const float (&x)[32], f32x2 U2, f32x2 M2, f32x2 (&ps)[2], uint32_t tP) {
     uint32_t p[16], l[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
         float d0, d1;
-        upk2(sub2(pk2(x[2 * k], x[2 * k + 1]), M2), d0, d1);
+        upk2(fma2(pk2(x[2 * k], x[2 * k + 1]), U2, M2), d0, d1);
         d0 = ex2(d0), d1 = ex2(d1);
         ps[k & 1] = add2(ps[k & 1], pk2(d0, d1));
         p[k] = h2(d0, d1);
@@ -323,7 +325,7 @@ __device__ __forceinline__ void next_segment(const Args &a, Walk<Cfg<kWide>::R, 
 template <bool kWide>
 __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned char *base, uint32_t tmem) {
     using C = Cfg<kWide>;
-    constexpr int NB = C::NB, KS = C::KS, R = C::R;
+    constexpr int KS = C::KS, R = C::R;
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, blk = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -336,37 +338,13 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
     while (!w.done()) {
         const Segment<kWide> g(a, w);
         const int wr = g.r0 + 32 * warp, n_rows = min(32, g.rows - wr);  // the warp's rows; may be none
+        float down = 1.0f;  // of this lane's row: its power of two
         {
-            // |q~| is at most the sum of |q| over a row, that is 32 times the largest sum over a lane
-            float m = 0.0f;
-            float v[8][4];
-            int row[8];  // a row behind the last one repeats it, and counts as zeros
-#pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += 8) {  // eight rows at a time, so that their loads overlap
-#pragma unroll
-                for (int r = 0; r < 8; ++r) row[r] = min(wr + r0 + r, g.rows - 1);
-                load_rows<8, !kWide>(a, g.s, g.head, row, lane, v);
-#pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const float x = __fadd_rn(__fadd_rn(fabsf(v[r][0]), fabsf(v[r][1])), __fadd_rn(fabsf(v[r][2]), fabsf(v[r][3])));
-                    m = x < INFINITY ? fmaxf(m, x) : m;  // a row that is not finite spoils only itself
-                }
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (lane == 0) sh.top[warp] = m;
-            named_sync<1, 128 * NB>();
-#pragma unroll
-            for (int i = 0; i < 4 * NB; ++i) m = fmaxf(m, sh.top[i]);
-            m = fminf(m, 0x1p120f);
-            // 2^u and 2^-u with u = kQBits - exponent of 32 m, by biased exponents
-            const int e = max(kQBits + 1, (int)(__float_as_uint(__fmul_rn(m, 32.0f)) >> 23));
-            const int up_exp = min(254, 254 + kQBits - e);
-            const float up = __uint_as_float((uint32_t)up_exp << 23);
-            if (tid == 0) sh.down = __uint_as_float((uint32_t)(254 - up_exp) << 23);
             unsigned char *const op = base + C::kOffQ + blk * C::kParts * kOp + (lane >> 4) * kBox + 8 * (lane & 1);
 #pragma unroll 1
-            for (int r0 = 0; r0 < 32; r0 += 8) {
+            for (int r0 = 0; r0 < 32; r0 += 8) {  // eight rows at a time, so that their loads and shuffles overlap
+                float v[8][4];
+                int row[8];  // a row behind the last one repeats it, and counts as zeros
 #pragma unroll
                 for (int r = 0; r < 8; ++r) row[r] = min(wr + r0 + r, g.rows - 1);
                 load_rows<8, !kWide>(a, g.s, g.head, row, lane, v);
@@ -375,6 +353,13 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[r][i] = r0 + r < n_rows ? __fmul_rn(v[r][i], sg[i]) : 0.0f;
                     row_fwht(v[r], lane);
+                    // 2^u and 2^-u that bring the largest |q~| to 2^kQBits, by biased exponents (1 where the
+                    // row is not finite)
+                    const float m = fmaxf(fmaxf(fabsf(v[r][0]), fabsf(v[r][1])), fmaxf(fabsf(v[r][2]), fabsf(v[r][3])));
+                    const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(m)) >> 23);
+                    const int up_exp = e == 255 ? 127 : min(253, 254 + kQBits - e);
+                    const float up = __uint_as_float((uint32_t)up_exp << 23);
+                    if (lane == r0 + r) down = __uint_as_float((uint32_t)(254 - up_exp) << 23);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[r][i] = __fmul_rn(v[r][i], up);
                     unsigned char *const to = op + ((warp & 3) * 32 + r0 + r) * 128 + (((lane >> 1 & 7) ^ r) << 4);
@@ -401,12 +386,14 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
             for (int i = 0; i < g.take && !dead; ++i) {
                 const uint32_t st = (n_tile + i) % KS;
                 const int j0 = g.span.tile(g.first + i) * kTileKeys;
-                if (!warp_wait(&sh.full_v[st], ((n_tile + i) / KS) & 1u)) {
+                if (!warp_wait(&sh.full_k[st], ((n_tile + i) / KS) & 1u) || !warp_wait(&sh.full_v[st], ((n_tile + i) / KS) & 1u)) {
                     dead = true;
                     break;
                 }
                 const Tile t = sh.tile[st];
                 G = t.G;
+                // from S to the logit in log2 units (at least 2^-126, so that -inf stays what it is)
+                const float unit = fmaxf(__fmul_rn(down, sh.unit[(n_tile + i) & 3]), 0x1p-126f);
                 const bool full = (t.valid[0] & t.valid[1] & t.valid[2] & t.valid[3]) == 0xffffffffu && j0 + kTileKeys <= lo + 1 &&
                                   (a.window == 0 || j0 > hi - a.window || j0 + kTileKeys <= a.sinks);
 #pragma unroll
@@ -430,19 +417,19 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
                             y[k] = (on1 >> k & 1u) ? y[k] : -INFINITY;
                         }
                     }
-                    const float mx = max32(max32(-INFINITY, x), y);
+                    const float mx = __fmul_rn(max32(max32(-INFINITY, x), y), unit);
                     if (__any_sync(0xffffffffu, mx > __fadd_rn(M, kLazy))) {  // every row of the warp takes its own maximum
                         const float m = fmaxf(M, mx), alpha = ex2(__fsub_rn(M, m));
                         M = m;
                         sum = __fmul_rn(sum, alpha);
                         scale = __fmul_rn(scale, alpha);
                     }
-                    const float Mo = __fsub_rn(M, kLift);
-                    const f32x2 M2 = pk2(Mo, Mo);
+                    const float Mo = __fsub_rn(kLift, M);
+                    const f32x2 M2 = pk2(Mo, Mo), U2 = pk2(unit, unit);
                     f32x2 ps[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
                     // P's columns lie over the half's columns of S
-                    weights<kWide>(x, M2, ps, tP + 64 * half);
-                    weights<kWide>(y, M2, ps, tP + 64 * half + (kWide ? 32 : 16));
+                    weights<kWide>(x, U2, M2, ps, tP + 64 * half);
+                    weights<kWide>(y, U2, M2, ps, tP + 64 * half + (kWide ? 32 : 16));
                     float s0, s1;
                     upk2(add2(ps[0], ps[1]), s0, s1);
                     sum = __fadd_rn(sum, __fadd_rn(s0, s1));
@@ -547,7 +534,7 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
     uint64_t *const full = values ? sh.full_v : sh.full_k, *const free = values ? sh.free_v : sh.free_k;
     const uint8_t *const pool = values ? a.pools.v : a.pools.k;
     bool dead = false;
-    uint32_t n_tile = 0, segs = 0;
+    uint32_t n_tile = 0;
     while (!w.done()) {
         const Segment<kWide> g(a, w);
         const int take = g.blind ? 0 : g.take;
@@ -588,8 +575,6 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
         ask(0);
         fetch(0);
         ask(1);
-        if (!values && take > 0 && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
-        const float coef = __fmul_rn(a.coef, sh.down);
 #pragma unroll 1
         for (int i = 0; i < take; ++i) {
             const uint32_t n = n_tile + i, st = n % KS, use = n / KS;
@@ -600,48 +585,50 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
                 recs + (i % kRecStages) * 2 * kRecBytes + key * tq3_cache::kRec);
             const float2 own = *reinterpret_cast<const float2 *>(rec + 12);
             float factor = __fmul_rn(own.x, own.y);
-            if (values) {
-                if (!(fabsf(factor) < INFINITY)) factor = 0.0f;
-                // the largest factor of the tile (the four warps leave together: a warp whose wait ran
-                // out says so here)
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(factor)));
-                if (lane == 0) sh.gmax[n & 1][warp & 3] = dead ? 0xffffffffu : top;
+            if (!values) factor = __fmul_rn(factor, a.coef);
+            const bool finite = fabsf(factor) < INFINITY;
+            if (values && !finite) factor = 0.0f;
+            // the largest finite factor of the tile (the four warps leave together: a warp whose wait ran out
+            // says so here)
+            const uint32_t top = __reduce_max_sync(0xffffffffu, finite ? __float_as_uint(fabsf(factor)) : 0u);
+            if (lane == 0) sh.most[n & 1][values][warp & 3] = dead ? 0xffffffffu : top;
+            if (values)
                 named_sync<2, 128>();
-                uint32_t all = 0;
+            else
+                named_sync<1, 128>();
+            uint32_t all = 0;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) all = max(all, sh.gmax[n & 1][x]);
-                if (all == 0xffffffffu) {
-                    dead = true;
-                    break;
-                }
-                const float most = __uint_as_float(all);
-                float ratio = 1.0f;
-                if (G == 0.0f || most > 4.0f * G) {
-                    // a power of two at or below it, within 2^-100 .. 2^126; O is rescaled by an exact ratio
-                    const float up = __uint_as_float(min(253u << 23, max(27u << 23, all & 0x7f800000u)));
+            for (int x = 0; x < 4; ++x) all = max(all, sh.most[n & 1][values][x]);
+            if (all == 0xffffffffu) {
+                dead = true;
+                break;
+            }
+            // a power of two at or below it, within 2^-100 .. 2^126
+            const float up = __uint_as_float(min(253u << 23, max(27u << 23, all & 0x7f800000u)));
+            const uint32_t valid = __ballot_sync(0xffffffffu, (have >> (i % kRecStages)) & 1u);
+            float ratio = 1.0f;
+            if (values) {
+                if (G == 0.0f || __uint_as_float(all) > 4.0f * G) {
                     if (up > G) {
-                        ratio = __fmul_rn(G, __uint_as_float((254u << 23) - __float_as_uint(up)));
+                        ratio = __fmul_rn(G, __uint_as_float((254u << 23) - __float_as_uint(up)));  // exact
                         G = up;
                     }
                 }
                 factor = __fmul_rn(factor, __fmul_rn(kVTop, __uint_as_float((254u << 23) - __float_as_uint(G))));
-                const uint32_t valid = __ballot_sync(0xffffffffu, (have >> (i % kRecStages)) & 1u);
-                if (n >= KS && !warp_wait(&free[st], (use - 1) & 1u)) {
-                    dead = true;
-                    continue;
-                }
-                if (lane == 0) {
-                    sh.tile[st].valid[warp & 3] = valid;
-                    if (warp == 12) sh.tile[st].ratio = ratio, sh.tile[st].G = G;
-                }
             } else {
                 const float2 other = *reinterpret_cast<const float2 *>(base + C::kOffFac + (i % kRecStages) * kTileKeys * 8 + key * 8);
-                factor = __fmul_rn(factor, coef);
+                factor = __fmul_rn(factor, __fmul_rn(kKTop, __uint_as_float((254u << 23) - __float_as_uint(up))));
                 if (!(fabsf(__fmul_rn(other.x, other.y)) < INFINITY)) factor = __uint_as_float(0x7fffffffu);
-                if (dead || (n >= KS && !warp_wait(&free[st], (use - 1) & 1u))) {
-                    dead = true;
-                    break;
-                }
+            }
+            if (n >= KS && !warp_wait(&free[st], (use - 1) & 1u)) {
+                dead = true;
+                continue;
+            }
+            if (lane == 0) {
+                Tile &t = sh.tile[st];
+                if (values) t.valid[warp & 3] = valid;
+                if (warp == 12) t.ratio = ratio, t.G = G;
+                if (warp == 8) sh.unit[n & 3] = __fmul_rn(up, 1.0f / kKTop);
             }
             expand<kWide>(ops + st * C::kParts * kOp, key, rec, factor);
             fence_proxy_async_smem();
@@ -649,7 +636,6 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
             if (lane == 0) mbar_arrive(&full[st]);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        ++segs;
         n_tile += take;
         next_segment<kWide>(a, w, false);
     }
