@@ -241,9 +241,10 @@ wq_status tq3_cache_read(const uint8_t *k_pool, const uint8_t *v_pool, int64_t n
  *   out        device, [n_tokens][q_heads][128] of out_dtype, 16-byte aligned.
  *   workspace  device, 16-byte aligned, tq3_attention_chunk_workspace(max_q, q_heads / kv_heads) bytes,
  *              contents unspecified before and after. Calls that may run at the same time need one each.
- * Precision: a logit is within (2^-11 + 2^-15) softmax_scale |q| |k_j| and each term of the value sum
- * within 2^-10 of its own where q and out are bf16 (a bf16 result is rounded by up to 2^-8); within
- * 2^-17 softmax_scale |q| |k_j|, and fp32 sums, where either is fp32. Sums are fp32, in an order that
+ * Precision: where q and out are bf16 the operands are rounded to fp16, and a logit is within
+ * (2^-10 + 2^-15) softmax_scale |q| |k_j| and each term of the value sum within 2^-10 of its own (a bf16
+ * result is rounded by up to 2^-8); where either is fp32 the operands are split in two, and they are within
+ * 2^-17 softmax_scale |q| |k_j| and 2^-19. Sums are fp32, in an order that
  * depends on the lengths alone. Record norms and scales are taken to be what the encoders write: not
  * negative, and a value vector shorter than 2^-100 may count as one of that length.
  * Errors: WQ_ERR_SHAPE (counts, strides, window or sinks out of range, softmax_scale not finite,
@@ -391,7 +392,8 @@ wq_status wq_rpbh_codebook(int bits, int64_t d, float *out);
  * leaving its outputs unspecified: bit 0 a TQ3 kernel waiting for a TMA tile, bit 1 an RPBH kernel
  * waiting for a row copy or the CUDA-core attention waiting for a tile's records, bit 3 the tensor-core TQ3 encoder waiting for a tile or its product,
  * bit 4 rpbh_linear waiting for a tile, the unpacked weights or its product, bit 5 the self-test
- * wq_selftest_wait_timeout, bit 7 the tensor-core attention waiting for its product. Bit 6 is not a wait: a call that takes slots or a page table
+ * wq_selftest_wait_timeout, bit 7 the tensor-core attentions (tq3_attention_chunk too) waiting for
+ * an operand or a product. Bit 6 is not a wait: a call that takes slots or a page table
  * met a slot or page-table entry outside the pool (that record was skipped,
  * decoded as zeros, or masked out of the attention; the rest of the call is complete).
  * Synchronous (a device-to-host copy on the legacy default stream); `flags` is host memory.
