@@ -4,16 +4,16 @@
 Tolerances, derived from the operands' roundings (u the half step of a type). A logit is
     s_ij = scale f_j post (q~_i . c[idx_j])        (q~ = H (signs . q), f_j = norm_j scale_j)
 and its abs sum A_ij = scale f_j post (|q~_i| . |c[idx_j]|). Where q and out are bf16 the operands are
-fp16: q~ is rounded by 2^-11, the centroids by 1.4e-5, and 8 fp32 accumulations plus the transform's 7
-roundings and a few of the factors (below 2^-16 together): |ds_ij| <= L A_ij with L = 2^-11 + 2^-15. A
-weight is off by that and by its own rounding, 2^-11, the value's centroid by 1.4e-5, exp2 and log2 by
-2^-21: e_ij = |ds_ij| + 2^-11 + 2^-15 relative, in the numerator; the denominator has ds_ij alone. So to
-first order
-    |out_i - exact| <= sum_j p_ij |ds_ij| |v_j - out_i| + sum_j p_ij (2^-11 + 2^-15) |v_j|
+fp16: q~ is rounded by 2^-11, the centroids by 1.4e-5 or, times the key's factor, by 2^-11, and the fp32
+accumulations, the transform's 7 roundings and a few of the factors stay below 2^-16 together:
+|ds_ij| <= L A_ij with L = 2^-10 + 2^-15. A weight is off by that, by its own rounding, 2^-11, and the
+value's operand by another 2^-11 (or 1.4e-5), exp2 and log2 by 2^-21; the denominator has ds_ij alone. So
+to first order
+    |out_i - exact| <= sum_j p_ij |ds_ij| |v_j - out_i| + sum_j p_ij (2^-10 + 2^-15) |v_j|
 in the 2-norm, to which 5% is added for the second order, and the bf16 result's 2^-8 |out_i|. Accumulating
 the values, n_i of them, costs at most (n_i / 16 + 32) 2^-22 sum_j p_ij |v_j|, a tensor-core accumulation
 taken as 2^-22. With fp32 on either side an operand is hi + lo, two roundings of 2^-11 (2^-22), the
-dropped lo lo another 2^-22: L = 2^-20 + 24 accumulations of 2^-22, and 2^-20 in place of 2^-11 + 2^-15.
+dropped lo lo another 2^-22: L = 2^-20 + 24 accumulations of 2^-22, and 2^-20 in place of 2^-10 + 2^-15.
 """
 import numpy as np
 import pytest
@@ -102,8 +102,8 @@ def check(out, q, cache, new, bits, wide, window=0, sinks=0, scale=128 ** -0.5, 
                 got = out[at:at + n, h * group + g].astype(np.float64)
                 vn = np.linalg.norm(v, axis=1)
                 dist = np.linalg.norm(v[None] - ref[:, None], axis=2)
-                lam = 2.0 ** -20 + 24 * 2.0 ** -22 if wide else 2.0 ** -11 + 2.0 ** -15
-                w = 2.0 ** -20 if wide else 2.0 ** -11 + 2.0 ** -15
+                lam = 2.0 ** -20 + 24 * 2.0 ** -22 if wide else 2.0 ** -10 + 2.0 ** -15
+                w = 2.0 ** -20 if wide else 2.0 ** -10 + 2.0 ** -15
                 count = seen.sum(1) * (3 if wide else 1)
                 bound = 1.05 * ((p * lam * np.where(seen, A, 0) * dist).sum(1) + w * (p @ vn))
                 bound += (count / 16 + 32) * 2.0 ** -22 * (p @ vn)
@@ -277,6 +277,51 @@ def test_magnitudes(wq, q_scale, kv_scale, new):
                                  torch.tensor([200], dtype=torch.int32, device="cuda"), wq.sign_mask_words(bits),
                                  softmax_scale=scale)
     check(to_np(out), q.cpu().numpy(), cache, [new], bits, True, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [1, 90])
+@pytest.mark.parametrize("keys_grow,values_grow", [(2.0, 8.0), (-2.0, -8.0), (0.0, 12.0)])
+def test_norms_that_grow_and_shrink(wq, new, dtype, keys_grow, values_grow):
+    """Factors that change by e^grow along the sequence, and by as much between neighbours for one key in
+    five: running maxima are raised, and values of very different length share a tile."""
+    bits = inputs.tq3_sign_bits()
+    n = 1100
+    cache = Cache([n], 1, 16, seed=15)
+    r = np.random.RandomState(16)
+    for pool, grow in zip(cache.pools, (keys_grow, values_grow)):
+        for j in range(n):
+            f = pool[cache.table[0, j // 16], 0, j % 16, 48:].view(np.float32)
+            f[0] *= np.exp(grow * (j / n - 0.5) + (r.uniform(-grow, grow) / 2 if j % 5 == 0 else 0.0))
+    pools, table = cache.device()
+    q = torch.from_numpy(inputs.gaussian((new, 4, 128), seed=4)).to(dtype).cuda()
+    out = wq.tq3_attention_chunk(q, *pools, table, torch.tensor([0, new], dtype=torch.int32, device="cuda"),
+                                 torch.tensor([n], dtype=torch.int32, device="cuda"), wq.sign_mask_words(bits))
+    check(to_np(out), q.float().cpu().numpy(), cache, [new], bits, dtype == F32)
+    assert wq.device_fault() == 0
+
+
+def test_two_streams_at_once(wq):
+    """Calls of both kernels on two streams, interleaved, give what each gives alone."""
+    bits = inputs.tq3_sign_bits()
+    m = wq.sign_mask_words(bits)
+    cache = Cache([900, 300, 700, 1200], 2, 16, seed=17)
+    pools, table = cache.device()
+    kv = torch.tensor(cache.keys, dtype=torch.int32, device="cuda")
+    new = [1, 70, 1, 200]
+    start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    qs = [torch.from_numpy(inputs.gaussian((sum(new), 8, 128), seed=s) * 0.3).to(BF16).cuda() for s in (1, 2)]
+    alone = [wq.tq3_attention_chunk(q, *pools, table, start, kv, m) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(wq.tq3_attention_chunk(qs[i], *pools, table, start, kv, m))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, alone[i]) for o in outs[i])
 
 
 @pytest.mark.parametrize("new", [1, 130])

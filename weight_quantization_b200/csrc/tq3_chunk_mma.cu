@@ -758,9 +758,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         if (tid == 0) {
             w = mine;
             cut->cut = 0;
-            if (blockIdx.x == 0)
-                for (int b = 0; b < a.batch; ++b)
-                    if (__ldg(a.kv_len + b) > a.max_keys) atomicOr(&g_fault, tq3::kFaultPoolIndex);
         }
     }
     tc_fence_before();
