@@ -2,9 +2,9 @@
 // (tq3_quantize, tq3_dequantize) on the pools of tq3_cache.cuh.
 //
 // Both kernels give a vector to one thread (64 packed fp32 pairs in registers, so the seven FWHT
-// stages need no exchange) and a tile of 32 tokens of one head of K or V to one warp, which is the
-// whole CTA. A tile's records are then one or a few runs of consecutive places in the pool, moved in
-// 8-byte pieces by neighbouring lanes; its rows are moved in 16-byte pieces through shared memory.
+// stages need no exchange) and a tile of 32 tokens of one head of K or V to one warp. A tile's
+// records are then one or a few runs of consecutive places in the pool, moved in 8-byte pieces by
+// neighbouring lanes; its rows are moved in 16-byte pieces through shared memory.
 //
 // append. With z = H (s . x) and m = max|z|: norm = max(|x|, 1e-8), scale = max(m / (sqrt(128) norm),
 // 1e-8), idx_i = #{k : B_k scale < z_i / (sqrt(128) norm)}. In exact arithmetic that is B_k T < z_i
@@ -30,8 +30,15 @@ namespace tq3_cache {
 using tq3::SignMask;
 
 constexpr int kTile = 32;      // tokens per tile = threads per CTA
-constexpr int kCtasPerSm = 12; // what 168 registers a thread and 18 KiB of shared memory allow
+// Both bodies are some 2500 instructions long, more than the instruction cache keeps for warps that are each
+// somewhere else in it. Append's 12 warps of an SM (what 168 registers a thread allow) are one CTA that meets
+// before each item and so shares its fetches: 32768 tokens x 8 heads take 113 us with a CTA a warp, 102 with
+// four warps a CTA, 86 with twelve, 92 where they meet twice an item. Read waits for its stores more than for
+// instructions and loses by it: 58, 63 and 74 us for 16 sequences of up to 4096 keys.
+constexpr int kAppendWarps = 12;
+constexpr int kReadCtas = 12;  // per SM, a warp each
 constexpr int kSms = 148;
+constexpr int kAppendBytes = 16384 + 32 * kRec;  // of a warp: two bf16 tiles or one fp32 tile, and the tile's records
 constexpr float kNear = 0.5f - 4.5e-5f;
 
 __device__ unsigned int g_fault;
@@ -140,19 +147,20 @@ static __device__ __noinline__ void encode_row_fp64(const unsigned char *row, co
 // append
 // ---------------------------------------------------------------------------------------------
 template <bool kBf16, bool kDefault>
-__global__ void __launch_bounds__(kTile, kCtasPerSm)
+__global__ void __launch_bounds__(kAppendWarps * 32, 1)
     append_kernel(Rows in, int64_t tokens, const int64_t *__restrict__ slots, Pools pools, SignMask mask) {
     constexpr int kRowBytes = kBf16 ? 256 : 512, kChunks = kRowBytes / 16;
     constexpr int kStages = kBf16 ? 2 : 1;
-    extern __shared__ __align__(16) unsigned char smem[];
+    extern __shared__ __align__(16) unsigned char smem_all[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned char *const smem = smem_all + warp * kAppendBytes;
     uint32_t *const recs = reinterpret_cast<uint32_t *>(smem + kStages * kTile * kRowBytes);  // [32][14]
-    const int lane = threadIdx.x;
     const int64_t n_slots = pools.n_pages << pools.shift;
-    // items: (tile of tokens, head, K or V), the last fastest; a contiguous share of them for each CTA
+    // items: (tile of tokens, head, K or V), the last fastest; a contiguous share of them for each warp
     const int per_tile = 2 * pools.heads;
     const int64_t items = (tokens + kTile - 1) / kTile * per_tile;
-    const int64_t begin = items * blockIdx.x / gridDim.x, end = items * (blockIdx.x + 1) / gridDim.x;
-    if (begin >= end) return;
+    const int64_t warps = (int64_t)gridDim.x * kAppendWarps, me = (int64_t)blockIdx.x * kAppendWarps + warp;
+    const int64_t begin = items * me / warps, end = items * (me + 1) / warps, rounds = (items + warps - 1) / warps;
 
     auto row_of = [&](int hk, int64_t token) {
         const int64_t head = hk >> 1;
@@ -170,9 +178,11 @@ __global__ void __launch_bounds__(kTile, kCtasPerSm)
 
     int64_t tile = begin / per_tile, have = -1, slot = -1;
     int hk = (int)(begin - tile * per_tile);
-    fetch(tile * kTile, hk, 0);
+    if (begin < end) fetch(tile * kTile, hk, 0);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    for (int64_t item = begin; item < end; ++item) {
+    for (int64_t item = begin; item < begin + rounds; ++item) {
+        __syncthreads();
+        if (item >= end) continue;
         const int stage = kStages == 2 ? (int)((item - begin) & 1) : 0;
         const int64_t t0 = tile * kTile, token = t0 + lane;
         if (have != tile) {
@@ -329,7 +339,7 @@ __device__ __forceinline__ int64_t place_of(const Dense &d, const Pools &p, int6
 }
 
 template <bool kBf16, bool kDefault>
-__global__ void __launch_bounds__(kTile, kCtasPerSm) read_kernel(Dense d, Pools pools, SignMask mask) {
+__global__ void __launch_bounds__(kTile, kReadCtas) read_kernel(Dense d, Pools pools, SignMask mask) {
     constexpr int kRowBytes = kBf16 ? 256 : 512, kChunks = kRowBytes / 16;
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x;
@@ -430,8 +440,15 @@ unsigned int read_and_clear_fault() {
     return v;
 }
 
-inline unsigned grid_for(int64_t items) {
-    const int64_t most = (int64_t)kSms * kCtasPerSm;
+template <typename... K, typename... A>
+wq_status launch(void (*kernel)(K...), unsigned grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), smem)) return WQ_ERR_CUDA;
+    kernel<<<grid, threads, smem, s>>>(args...);
+    return launch_status();
+}
+
+inline unsigned grid_for(int64_t items, int per_sm) {
+    const int64_t most = (int64_t)kSms * per_sm;
     return (unsigned)(items < most ? items : most);
 }
 
@@ -465,19 +482,19 @@ extern "C" wq_status tq3_cache_append(const void *k, const void *v, int dtype, i
     const tq3_cache::Rows rows{static_cast<const unsigned char *>(k), static_cast<const unsigned char *>(v),
                                k_token_stride * size, k_head_stride * size, v_token_stride * size,
                                v_head_stride * size};
-    const unsigned grid = tq3_cache::grid_for((tokens + 31) / 32 * kv_heads * 2);
-    const size_t smem = 16384 + 32 * 56;  // two bf16 tiles or one fp32 tile, and the tile's records
+    const unsigned grid = tq3_cache::grid_for((tokens + 31) / 32 * kv_heads * 2, 1);
+    using namespace tq3_cache;
+    constexpr int threads = 32 * kAppendWarps;
+    const size_t smem = kAppendWarps * kAppendBytes;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool def = tq3::is_default(m);
     if (dtype == WQ_BF16 && def)
-        tq3_cache::append_kernel<true, true><<<grid, 32, smem, s>>>(rows, tokens, slots, pools, m);
-    else if (dtype == WQ_BF16)
-        tq3_cache::append_kernel<true, false><<<grid, 32, smem, s>>>(rows, tokens, slots, pools, m);
-    else if (def)
-        tq3_cache::append_kernel<false, true><<<grid, 32, smem, s>>>(rows, tokens, slots, pools, m);
-    else
-        tq3_cache::append_kernel<false, false><<<grid, 32, smem, s>>>(rows, tokens, slots, pools, m);
-    return launch_status();
+        return launch(append_kernel<true, true>, grid, threads, smem, s, rows, tokens, slots, pools, m);
+    if (dtype == WQ_BF16)
+        return launch(append_kernel<true, false>, grid, threads, smem, s, rows, tokens, slots, pools, m);
+    if (def)
+        return launch(append_kernel<false, true>, grid, threads, smem, s, rows, tokens, slots, pools, m);
+    return launch(append_kernel<false, false>, grid, threads, smem, s, rows, tokens, slots, pools, m);
 }
 
 extern "C" wq_status tq3_cache_read(const uint8_t *k_pool, const uint8_t *v_pool, int64_t n_pages, int64_t kv_heads,
@@ -501,17 +518,15 @@ extern "C" wq_status tq3_cache_read(const uint8_t *k_pool, const uint8_t *v_pool
                                  tq3_cache::page_shift(page_size)};
     const tq3_cache::Dense d{static_cast<unsigned char *>(k_out), static_cast<unsigned char *>(v_out), n_tokens,
                              page_table, seq_start, batch, pages_per_seq};
-    const unsigned grid = tq3_cache::grid_for((n_tokens + 31) / 32 * kv_heads * 2);
+    const unsigned grid = tq3_cache::grid_for((n_tokens + 31) / 32 * kv_heads * 2, tq3_cache::kReadCtas);
     const size_t smem = 32 * (out_dtype == WQ_BF16 ? 256 : 512);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool def = tq3::is_default(m);
     if (out_dtype == WQ_BF16 && def)
-        tq3_cache::read_kernel<true, true><<<grid, 32, smem, s>>>(d, pools, m);
-    else if (out_dtype == WQ_BF16)
-        tq3_cache::read_kernel<true, false><<<grid, 32, smem, s>>>(d, pools, m);
-    else if (def)
-        tq3_cache::read_kernel<false, true><<<grid, 32, smem, s>>>(d, pools, m);
-    else
-        tq3_cache::read_kernel<false, false><<<grid, 32, smem, s>>>(d, pools, m);
-    return launch_status();
+        return tq3_cache::launch(tq3_cache::read_kernel<true, true>, grid, 32, smem, s, d, pools, m);
+    if (out_dtype == WQ_BF16)
+        return tq3_cache::launch(tq3_cache::read_kernel<true, false>, grid, 32, smem, s, d, pools, m);
+    if (def)
+        return tq3_cache::launch(tq3_cache::read_kernel<false, true>, grid, 32, smem, s, d, pools, m);
+    return tq3_cache::launch(tq3_cache::read_kernel<false, false>, grid, 32, smem, s, d, pools, m);
 }
