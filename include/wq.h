@@ -235,8 +235,9 @@ wq_status tq3_cache_read(const uint8_t *k_pool, const uint8_t *v_pool, int64_t n
  *              below n_pages is masked out and sets device fault bit 6, and so does a kv_len beyond
  *              pages_per_seq * page_size (which then counts as that many keys).
  *   q_start, kv_len  device, (batch + 1) and batch x int32, 4-byte aligned, q_start ascending.
- *   max_q      how many new tokens a sequence has at most, to choose kernels and the workspace by; a
- *              sequence with more is served all the same.
+ *   max_q      how many new tokens a sequence has at most, to choose kernels and the workspace by (and so
+ *              does pages_per_seq * page_size, where that leaves little work); a sequence with more is
+ *              served all the same.
  *   window     0: none. sinks: first keys that a window leaves visible.
  *   out        device, [n_tokens][q_heads][128] of out_dtype, 16-byte aligned.
  *   workspace  device, 16-byte aligned, tq3_attention_chunk_workspace(max_q, q_heads / kv_heads) bytes,

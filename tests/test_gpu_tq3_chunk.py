@@ -38,6 +38,15 @@ def wq():
     return ops
 
 
+ROOM = 240000  # keys that a test's table has room for: with less, few rows choose the kernel for few rows
+
+
+def widened(table, page_size, room=ROOM):
+    """The table on the device, its rows widened by entries that no token needs."""
+    more = max(0, room // page_size - table.shape[1])
+    return torch.from_numpy(np.pad(table, ((0, 0), (0, more)), constant_values=-1)).cuda()
+
+
 class Cache:
     """Pools of random records, one page table, on the host and on the device."""
 
@@ -58,8 +67,8 @@ class Cache:
         for b, n in enumerate(need):
             self.table[b, :n], order = order[:n], order[n:]
 
-    def device(self):
-        return [torch.from_numpy(p).cuda() for p in self.pools], torch.from_numpy(self.table).cuda()
+    def device(self, room=ROOM):
+        return [torch.from_numpy(p).cuda() for p in self.pools], widened(self.table, self.page_size, room)
 
     def dense(self, which, b, h, n):
         """(norm * scale, centroids [n, 128]) of keys 0 .. n - 1; zeros without a page, and which have one."""
@@ -121,9 +130,9 @@ def to_np(t):
     return t.cpu().numpy() if t.dtype == F32 else t.float().cpu().numpy().astype(np.float64)
 
 
-def run(wq, cache, new, group, dtype=BF16, out_dtype=None, window=0, sinks=0, seed=1, q_scale=0.3, sign_seed=42, max_q=None):
+def run(wq, cache, new, group, dtype=BF16, out_dtype=None, window=0, sinks=0, seed=1, q_scale=0.3, sign_seed=42, max_q=None, room=ROOM):
     bits = inputs.tq3_sign_bits(sign_seed)
-    pools, table = cache.device()
+    pools, table = cache.device(room)
     n = sum(new)
     q = torch.from_numpy(inputs.gaussian((n, cache.heads * group, 128), seed=seed) * q_scale).to(dtype).cuda()
     start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
@@ -150,6 +159,13 @@ def test_against_the_definition(wq, keys, new, heads, group, page_size, dtype):
 @pytest.mark.parametrize("new", [(1, 1, 1), (40, 1, 7)])
 def test_window_and_sinks(wq, window, sinks, new, dtype):
     run(wq, Cache([700, 450, 9], 2, 16, seed=3), list(new), 4, dtype, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 3)])
+def test_little_work_in_blocks_of_eight_rows(wq, window, sinks, dtype):
+    """A narrow table: a chunk of many rows on the kernel for few."""
+    run(wq, Cache([300, 77], 2, 16, seed=18), [60, 1], 4, dtype, window=window, sinks=sinks, room=0)
 
 
 @pytest.mark.parametrize("dtype,out_dtype", [(BF16, F32), (F32, BF16)])
@@ -375,7 +391,7 @@ def test_offsets_past_32_bits(wq):
     for new in ([1, 1], [100, 3]):
         q = torch.from_numpy(inputs.gaussian((sum(new), 8, 128), seed=4) * 0.3).cuda()
         start = torch.tensor([0, new[0], sum(new)], dtype=torch.int32, device="cuda")
-        out = wq.tq3_attention_chunk(q, *pools, torch.from_numpy(table).cuda(), start,
+        out = wq.tq3_attention_chunk(q, *pools, widened(table, page_size), start,
                                      torch.tensor([300, 140], dtype=torch.int32, device="cuda"),
                                      wq.sign_mask_words(bits))
         check(to_np(out), q.cpu().numpy(), small, new, bits, True)
@@ -392,7 +408,7 @@ def test_a_serving_run(wq):
     order = torch.randperm(30, generator=torch.Generator().manual_seed(1))[:2 * width]
     cache = Cache([0, 0], heads, page_size)
     cache.pages, cache.table = 30, order.view(2, width).to(torch.int32).numpy()
-    table = torch.from_numpy(cache.table).cuda()
+    table = widened(cache.table, page_size)
     lengths = [0, 0]
     for step, new in enumerate([(70, 5), (1, 60), (1, 1), (30, 1), (1, 1)]):
         n = sum(new)

@@ -651,7 +651,16 @@ extern "C" wq_status tq3_attention_chunk(const void *q, int q_dtype, int64_t n_t
     a.ws = static_cast<unsigned char *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool wide = !a.q_bf16 || !a.out_bf16;
-    const bool few = max_q <= tq3_chunk::kFewRows / group;
+    // Blocks of 8 rows share no decoding, and the tensor-core kernel takes 256 rows with one: a tile of 128 keys
+    // costs the former 0.9 us of an SM per 8 rows, the latter 2.6 us whatever the rows are. But the latter also
+    // needs some 25 us to set up, transform, join and drain, so it is left out where no sequence has more than
+    // 8 rows, and where so little work is left (as far as the host knows: the tables' room stands for the
+    // lengths) that the former has three steps a CTA at most, one for split operands. 8 x 4 heads, 32 tokens
+    // over 515 keys: 24 us against 35; 64 tokens: 32 against 37; 32 over 1500: 29 against 39; fp32, 3 x up to 37
+    // tokens over 1531 keys, 4 heads: 28 against 43.
+    const int64_t blocks = (n_tokens * group + 7) / 8 + batch;
+    const double tiles = (double)blocks * (double)kv_heads * (double)((a.max_keys + 127) / 128);
+    const bool few = max_q <= tq3_chunk::kFewRows / group || tiles <= (wide ? 1 : 3) * tq3_chunk::kParts;
     if (!few) a.rows_to = tq3_chunk::kFewRows + 1;
     const wq_status st = wide ? tq3_chunk::run_rows<1, true>(a, s) : tq3_chunk::run_rows<1, false>(a, s);
     if (st != WQ_OK) return st;
