@@ -9,7 +9,7 @@
 // so both products are over centroids alone: 8 values, looked up as pairs (6 bits) in a table that
 // every lane has a column of in shared memory (a bank of its own, so no conflict).
 //
-// The rows kernel: a warp takes 32 keys at a time and one to NT times 8 rows of one KV head.
+// The rows kernel: a warp takes 32 keys at a time and 8 rows (NT is 1) of one KV head.
 // S^T = C_K q~^T and O^T += C_V^T w with m16n8k16: the looked-up pairs are the A operands as they are
 // (the 128 coordinates may be summed in any order, so a lane takes the coordinates whose bits it can
 // read as whole words), and no decoded key or value ever leaves the registers. In log2 units the
@@ -19,9 +19,15 @@
 //
 // Operands are fp16: the centroids times kGain are within 1.4e-5 of fp16 numbers, q~ is scaled by a
 // power of two per block of rows and rounded (2^-11 of each coordinate at most, so a logit moves by
-// 2^-11 softmax_scale |q| |k_j| at most), w likewise (2^-11 of a term). A bf16 result is rounded to 2^-8 afterwards. For
-// fp32 queries or results every operand is split into fp16 hi + lo (2^-22) and a product takes three
-// passes, hi hi + hi lo + lo hi. Sums are fp32.
+// 2^-11 softmax_scale |q| |k_j| at most), w likewise (2^-11 of a term). A bf16 result is rounded to 2^-8
+// afterwards. For fp32 queries or results every operand is split into fp16 hi + lo (2^-22) and a product
+// takes three passes, hi hi + hi lo + lo hi. Sums are fp32.
+//
+// Measured: one token of 8 sequences of 32768 keys, 8 KV heads x 4 rows, bf16: 97.6 us with the join, 2.4 TB/s
+// of records where a copy reaches 6.55. A step of 32 keys is 983 warp instructions, of which the 128 lookups
+// are 500; the issue slots are 67% busy, the ALU 61%, the shared-memory pipe 58%, the tensor cores 17%. Three
+// CTAs of more registers in place of four take as long; right shifts as high halves of multiplications, to
+// spare the ALU, 108 us; keys ordered so that no record read meets a bank twice, no change.
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math.h>
@@ -152,7 +158,8 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const uint8_t *src, uint
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ int64_t shfl64(int64_t v, int from) {
-    const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)v, from), hi = __shfl_sync(0xffffffffu, (uint32_t)((uint64_t)v >> 32), from);
+    const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)v, from),
+                   hi = __shfl_sync(0xffffffffu, (uint32_t)((uint64_t)v >> 32), from);
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
@@ -222,8 +229,9 @@ struct Steps {
     __device__ __forceinline__ uint32_t copy_pieces(const Args &a, int st, int p, int lane) const {
         const int64_t a0 = shfl64(at, p), a1 = shfl64(at, p + 1);
         const uint32_t b0 = a0 >= 0 ? 16 : 0, b1 = a1 >= 0 ? 16 : 0;  // nothing is read for 0 bytes
-        const uint8_t *const k0 = a.pools.k + (a0 >= 0 ? a0 : 0) + 16 * lane, *const k1 = a.pools.k + (a1 >= 0 ? a1 : 0) + 16 * lane;
-        const uint8_t *const v0 = a.pools.v + (a0 >= 0 ? a0 : 0) + 16 * lane, *const v1 = a.pools.v + (a1 >= 0 ? a1 : 0) + 16 * lane;
+        const int64_t o0 = (a0 >= 0 ? a0 : 0) + 16 * lane, o1 = (a1 >= 0 ? a1 : 0) + 16 * lane;
+        const uint8_t *const k0 = a.pools.k + o0, *const k1 = a.pools.k + o1;
+        const uint8_t *const v0 = a.pools.v + o0, *const v1 = a.pools.v + o1;
         const uint32_t dst = stage + st * kStageBytes + 16 * lane;
         cp_async16(dst, k0, b0);
         cp_async16(dst + 512, lane < 24 ? k0 + 512 : k1 + 512 - kPieceBytes, lane < 24 ? b0 : b1);
@@ -640,8 +648,8 @@ extern "C" wq_status tq3_attention_chunk(const void *q, int q_dtype, int64_t n_t
     a.table = page_table, a.q_start = q_start, a.kv_len = kv_len, a.pages_per_seq = pages_per_seq;
     a.batch = (int)batch, a.n_tokens = (int)n_tokens;
     tq3_chunk::set_group(a, (int)group);
-    const int64_t room = pages_per_seq > (tq3_chunk::kMaxKeys >> a.pools.shift) ? tq3_chunk::kMaxKeys : pages_per_seq << a.pools.shift;
-    a.max_keys = (int)room;
+    a.max_keys = pages_per_seq > (tq3_chunk::kMaxKeys >> a.pools.shift) ? tq3_chunk::kMaxKeys
+                                                                        : (int)(pages_per_seq << a.pools.shift);
     a.window = (int)window, a.sinks = (int)sinks;
     a.rows_from = 0, a.rows_to = INT32_MAX;
     // post * softmax_scale * log2(e), rounded once

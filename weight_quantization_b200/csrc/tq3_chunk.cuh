@@ -100,7 +100,7 @@ __device__ __forceinline__ Span block_span(const Args &a, const Seq &s, int bloc
     return span_of(a, before + token_of(a, r0), before + token_of(a, r1));
 }
 
-// On the line a segment is kSetup units, what loading its queries and storing its results costs in tiles,
+// On the line a segment is setup_units, what loading its queries and storing its results costs in tiles,
 // and then its tiles; who has the first tile begins it. A block without a visible key still counts one
 // tile: its rows are written as zeros.
 template <int R>
@@ -119,8 +119,8 @@ __device__ __forceinline__ int64_t tiles_of_head(const Args &a, const Seq &s) {
     return n;
 }
 
-// Part c of n is [begin(c), begin(c + 1)), the first total % n parts one tile longer. There are as many
-// parts as CTAs, or one per tile where there are fewer tiles: none is empty.
+// Part c of n is [begin(c), begin(c + 1)), the first total % n parts one unit longer. There are as many
+// parts as CTAs, or one per unit of the line where it is shorter.
 struct Line {
     int64_t each;
     int rest, parts;

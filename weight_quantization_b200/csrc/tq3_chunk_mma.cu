@@ -26,6 +26,14 @@
 // For fp32 queries or results the operands are split hi + lo, a product takes three passes (hi hi, hi lo,
 // lo hi), and 128 rows and one stage of operands fill the shared memory.
 //
+// Measured, with the join: 2048 tokens over 16384 keys, 8 KV heads x 4 rows a token, bf16: 606-658 us, 780-850
+// TFLOP/s, about half of what a library product reaches. A tile and 256 rows take some 4500 cycles, of which the
+// products need 2200 and the exponentials (MUFU) 2050; the softmax of a half tile takes 2500 to 3000, half of it
+// waits for tensor memory and barriers, with 60% of the issue slots busy. 256 rows a CTA because each decoded
+// operand then serves two products; with halves of 64 keys a block's softmax and its products overlap (697 us
+// without). Loops are rolled where they can be: code that runs once a segment is fetched anew each time, and at
+// 170 KB the kernel took 1220 us.
+//
 // Every wait is bounded; one that runs out sets fault bit 7, ends its role, and the others run out after
 // it. In-flight products get a bounded chance to finish before the tensor memory is freed.
 #include <cuda_runtime.h>
