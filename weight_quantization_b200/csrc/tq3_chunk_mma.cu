@@ -394,14 +394,13 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
             for (int i = 0; i < g.take && !dead; ++i) {
                 const uint32_t st = (n_tile + i) % KS;
                 const int j0 = g.span.tile(g.first + i) * kTileKeys;
-                if (!warp_wait(&sh.full_k[st], ((n_tile + i) / KS) & 1u) || !warp_wait(&sh.full_v[st], ((n_tile + i) / KS) & 1u)) {
+                if (!warp_wait(&sh.full_v[st], ((n_tile + i) / KS) & 1u)) {
                     dead = true;
                     break;
                 }
                 const Tile t = sh.tile[st];
                 G = t.G;
-                // from S to the logit in log2 units (at least 2^-126, so that -inf stays what it is)
-                const float unit = fmaxf(__fmul_rn(down, sh.unit[(n_tile + i) & 3]), 0x1p-126f);
+                float unit = 1.0f;  // from S to the logit in log2 units
                 const bool full = (t.valid[0] & t.valid[1] & t.valid[2] & t.valid[3]) == 0xffffffffu && j0 + kTileKeys <= lo + 1 &&
                                   (a.window == 0 || j0 > hi - a.window || j0 + kTileKeys <= a.sinks);
 #pragma unroll
@@ -411,6 +410,8 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
                         break;
                     }
                     tc_fence_after();
+                    // at least 2^-126, so that -inf stays what it is
+                    if (half == 0) unit = fmaxf(__fmul_rn(down, sh.unit[(n_tile + i) & 3]), 0x1p-126f);
                     tmem_ld32(tS + 64 * half, x);
                     tmem_ld32(tS + 64 * half + 32, y);
                     float scale = half ? 1.0f : t.ratio;  // of O, before this half's product
@@ -712,6 +713,9 @@ __device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned c
                         }
                     }
                     mma_commit(&sh.s_done[blk][half]);
+                    // Hands on what the decoding warps wrote with the keys (`unit`). The softmax must not wait
+                    // for the keys' own barrier: the tile two further may already have completed it again.
+                    if (half == 0) mbar_arrive(&sh.s_done[blk][0]);
                     if (half) mma_commit(&sh.free_k[st]);
                 }
                 if (nb < C::NB && half) {  // a block without rows frees its share
@@ -745,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             mbar_init(&sh.free_k[i], NB);
             mbar_init(&sh.free_v[i], NB);
             for (int h = 0; h < 2; ++h) {
-                mbar_init(&sh.s_done[i][h], 1);
+                mbar_init(&sh.s_done[i][h], h == 0 ? 2 : 1);
                 mbar_init(&sh.p_ready[i][h], 4);
             }
             mbar_init(&sh.pv_done[i], 1);
