@@ -191,10 +191,12 @@ struct Walk {
         if ((int)blockIdx.x >= line.parts) return;
         at = line.begin(blockIdx.x);
         end = line.begin(blockIdx.x + 1);
-        // the sequence that holds `at`: prefix sums
+        // the sequence that holds `at`: prefix sums (all of this ends, with valid places, even if the lengths
+        // change under the call)
+        if (tid == 0) scratch[kWarps] = -1;
         int64_t before = 0;
 #pragma unroll 1
-        for (int base = 0;; base += kThreads) {
+        for (int base = 0; base < a.batch; base += kThreads) {
             const int i = base + tid;
             Seq s;
             s.start = s.new_tokens = s.keys = 0;
@@ -228,6 +230,10 @@ struct Walk {
         }
         __syncthreads();
         b = (int)scratch[kWarps];
+        if (b < 0) {
+            seg = end = 0;
+            return;
+        }
         int64_t off = scratch[kWarps + 1];
         seq.start = (int)(scratch[kWarps + 2] >> 32);
         seq.new_tokens = (int)scratch[kWarps + 2];
@@ -236,13 +242,13 @@ struct Walk {
         const int64_t per_head = tiles_of_head<R>(a, seq);
         head = 0;
 #pragma unroll 1
-        for (; off >= per_head; off -= per_head) ++head;
+        for (; off >= per_head && head + 1 < a.pools.heads; off -= per_head) ++head;
         block = 0;
 #pragma unroll 1
         for (;; ++block) {
             span = block_span<R>(a, seq, block);
             const int n = max(1, span.n) + setup_units<R>();
-            if (off < n) break;
+            if (off < n || block + 1 >= blocks) break;
             off -= n;
         }
         seg = at - off;
@@ -279,6 +285,10 @@ struct Walk {
                     head = 0;
 #pragma unroll 1
                     do {
+                        if (b + 1 >= a.batch) {
+                            seg = end;
+                            return;
+                        }
                         seq = load_seq(a, ++b);
                     } while (seq.new_tokens == 0);
                     blocks = blocks_of<R>(a, seq);
