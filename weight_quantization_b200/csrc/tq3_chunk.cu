@@ -17,8 +17,8 @@
 // exponent, keeps w within fp16's range whatever the norms are, and leaves sum_j w_ij / g_j as the
 // softmax's denominator. M_i is raised only when it is passed by 2^8.
 //
-// Operands are fp16: the centroids times kGain are within 1.4e-5 of fp16 numbers, q~ is scaled by a
-// power of two per block of rows and rounded (2^-11 of each coordinate at most, so a logit moves by
+// Operands are fp16: the centroids times kGain are within 1.4e-5 of fp16 numbers, a row of q~ is scaled by a
+// power of two of its own and rounded (2^-11 of each coordinate at most, so a logit moves by
 // 2^-11 softmax_scale |q| |k_j| at most), w likewise (2^-11 of a term). A bf16 result is rounded to 2^-8
 // afterwards. For fp32 queries or results every operand is split into fp16 hi + lo (2^-22) and a product
 // takes three passes, hi hi + hi lo + lo hi. Sums are fp32.
@@ -73,8 +73,8 @@ struct Layout {
     static constexpr int kOffFactor = kOffStage + kWarps * kWarpBytes;  // per warp and key of a step
     static constexpr int kOffQ = kOffFactor + kWarps * kSub * 16;
     static constexpr int kOffStat = kOffQ + (kWide ? 2 : 1) * kQ * 2;  // per warp and row: M, l
-    static constexpr int kOffTop = kOffStat + kWarps * kRows * 8;      // per row: max |q~|
-    static constexpr int kOffInfo = kOffTop + kRows * 4;               // per warp and stage
+    static constexpr int kOffDown = kOffStat + kWarps * kRows * 8;     // per row: from its fp16 q~ to q~, times 2^-12
+    static constexpr int kOffInfo = kOffDown + kRows * 4;              // per warp and stage
     static constexpr int kOffScratch = kOffInfo + kWarps * kStages * 8;
     static constexpr int kBytes = kOffScratch + (kWarps + 4) * 8;
     static_assert(kRows * 132 * 4 <= kWarpBytes, "a warp's sums fit its stages");
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
     __half *const qs = reinterpret_cast<__half *>(smem + L::kOffQ);
     float4 *const factor = reinterpret_cast<float4 *>(smem + L::kOffFactor) + warp * kSub;
     float *const stat = reinterpret_cast<float *>(smem + L::kOffStat);
-    float *const top = reinterpret_cast<float *>(smem + L::kOffTop);
+    float *const downs = reinterpret_cast<float *>(smem + L::kOffDown);
 
     for (int i = tid; i < 64 * 32; i += kThreads) {
         const uint32_t f = i >> 5;
@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
         steps.begin(w, p_hi);
         steps.request(a, w, warp, lane, kAhead);
 
-        // q~ of the block's rows, scaled by the power of two that brings the largest to 2^13 .. 2^14
-        float down;
+        // q~ of the block's rows, each scaled by the power of two that brings its largest to 2^13 .. 2^14 (1 where
+        // it is not finite): a row keeps its bits whatever the size of the others
         {
             constexpr int kEach = R / kWarps;
             float v[kEach][4];
@@ -326,27 +326,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[n][i] = r0 + r < rows ? __fmul_rn(v[n][i], sg[i]) : 0.0f;
                 row_fwht(v[n], lane);
-                float m = fmaxf(fmaxf(fabsf(v[n][0]), fabsf(v[n][1])), fmaxf(fabsf(v[n][2]), fabsf(v[n][3])));
-#pragma unroll
-                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                if (lane == 0) top[r] = m < INFINITY ? m : 0.0f;  // such a row spoils only itself
-            }
-            __syncthreads();
-            float m = 0.0f;
-#pragma unroll
-            for (int r = 0; r < R; ++r) m = fmaxf(m, top[r]);
-            // 2^(13 - e) and its reciprocal, of biased exponents 267 - e and e - 13 (up to 2^127)
-            const int e = max(14, min(253, (int)(__float_as_uint(m) >> 23)));
-            const int up_exp = min(254, 267 - e);
-            const float up = __uint_as_float((uint32_t)up_exp << 23);
-            down = __uint_as_float((uint32_t)(254 - up_exp) << 23);
-#pragma unroll
-            for (int n = 0; n < kEach; ++n) {
+                const float m = fmaxf(fmaxf(fabsf(v[n][0]), fabsf(v[n][1])), fmaxf(fabsf(v[n][2]), fabsf(v[n][3])));
+                const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(m)) >> 23);
+                const int up_exp = e == 255 ? 127 : min(253, 267 - e);
+                const float up = __uint_as_float((uint32_t)up_exp << 23);
+                if (lane == 0) downs[r] = __fmul_rn(__uint_as_float((uint32_t)(254 - up_exp) << 23), 0x1p-12f);
                 float x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[i] = __fmul_rn(v[n][i], up);
                 uint2 hi = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
-                __half *const to = qs + (kWarps * n + warp) * 136 + 4 * lane;
+                __half *const to = qs + r * 136 + 4 * lane;
                 *reinterpret_cast<uint2 *>(to) = hi;
                 if (kWide)
                     *reinterpret_cast<uint2 *>(to + L::kQ) =
@@ -354,10 +343,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
             }
             __syncthreads();
         }
-        const float coef = __fmul_rn(__fmul_rn(a.coef, 1.0f / kGain), down);
+        // (2^12 with the key's factor and 2^-12 with the row's, so that the row's times S stays finite)
+        const float coef = __fmul_rn(a.coef, 4096.0f / kGain);
         // lane (g, t): row g, coordinates 32 t .. 32 t + 31, as the B operands of eight products
         uint32_t qh[NT][8][2], ql[NT][kWide ? 8 : 1][2];
-        int p[NT][2];  // positions of rows 2 t and 2 t + 1
+        int p[NT][2];  // of rows 2 t and 2 t + 1: positions, scales
+        float down[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const __half *const from = qs + (8 * n + g) * 136 + 32 * t;
@@ -374,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
             for (int e = 0; e < 2; ++e) {
                 const int r = r0 + 8 * n + 2 * t + e;
                 p[n][e] = r < rows ? before + token_of(a, r) : -1;
+                down[n][e] = downs[8 * n + 2 * t + e];
             }
         }
         // the first and the second three bytes of a lane's 48 bits in the two words that hold them
@@ -436,9 +428,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        S[x][n][e] = __fmaf_rn(S[x][n][e], e < 2 ? fa.x : fb.x, e < 2 ? fa.y : fb.y);
-                        live[x][n][e] = e < 2 ? fa.z : fb.z;
+                    for (int e = 0; e < 4; e += 2) {
+                        const float4 f = e == 0 ? fa : fb;
+                        float s0, s1;
+                        upk2(mul2(pk2(S[x][n][e], S[x][n][e + 1]), pk2(down[n][0], down[n][1])), s0, s1);
+                        S[x][n][e] = __fmaf_rn(s0, f.x, f.y);
+                        S[x][n][e + 1] = __fmaf_rn(s1, f.x, f.y);
+                        live[x][n][e] = live[x][n][e + 1] = f.z;
                     }
             }
             if (!(j0 + kSub <= p_lo + 1 && (a.window == 0 || j0 > p_hi - a.window || j0 + kSub <= a.sinks))) {
