@@ -3,13 +3,15 @@
 // segment has NB x 128 rows and a tile of 128 keys is two products per 128 rows:
 //     S = Q~ K^T       (128 rows x 128 keys, K = 128 rotated coordinates; both operands in shared memory)
 //     O += P V         (128 rows x 128 coordinates, K = 128 keys; P in tensor memory, V in shared memory)
-// with K's row j = c[idx_j] f_j coef 2^4 / F and V's row j = c[idx'_j] g_j 2^13 / G in fp16, F the power of
+// with K's row j = c[idx_j] f_j coef 2^13 / F and V's row j = c[idx'_j] g_j 2^13 / G in fp16, F the power of
 // two at the tile's largest f_j coef, and each row of q~ scaled by a power of two to 2^7 .. 2^8: one factor per
-// row and tile leads from S to the logit in log2 units, and it rides on the subtraction of the maximum. What
-// underflows in K then moves a logit by less than 2^-20 of the tile's largest. G follows the largest g_j of the
-// tiles so far and is raised when one is passed by 4 (O is rescaled then), so a value keeps all its bits down to
-// 2^-27 of the largest. A value whose factor is not finite becomes zero and poisons its key's logits
-// instead: a row that sees it gets NaN, any other is not touched.
+// row and tile leads from S to the logit in log2 units, and it rides on the subtraction of the maximum. G follows
+// the largest g_j of the tiles so far and is raised when one is passed by 4 (O is rescaled then). The least
+// centroid, 0.1129, leaves fp16's normal range where its factor is 2^-23 of F or G; below that a coordinate is
+// off by 2^-25, which moves a logit by 2^-34 softmax_scale |q| |k| at most, k the longest key of the tile, and the
+// result by 2^-34 of the longest value (the low halves of split operands reach that from 2^-12 on). Weights are
+// off by 2^-31 of the row's largest at most. A value whose factor is not finite becomes zero and poisons its
+// key's logits instead: a row that sees it gets NaN, any other is not touched.
 //
 // One CTA of 20 warps per SM. Warps 0-3 and 4-7 are the softmax of rows 0-127 and 128-255: a thread a row,
 // which lies in its tensor-memory lane. Warps 8-11 decode keys and 12-15 values: a thread a record. Warps 16
@@ -67,8 +69,8 @@ constexpr float kLazy = 8.0f, kLift = 6.0f;  // as in tq3_chunk.cu
 constexpr int kRecBytes = kTileKeys * tq3_cache::kRec;  // a tile's records of one pool
 constexpr int kRecStages = 2;
 constexpr int kQBits = 7;             // the largest |q~| of a row is scaled to 2^7 .. 2^8
-constexpr float kKTop = 16.0f;        // a key of a factor that is the largest power of two in the tile has this one
-constexpr float kVTop = 8192.0f;      // a value of factor G has this one
+// A key of factor F has this one, and a value of factor G: factors are below 4 of those, so operands below 2^15.
+constexpr float kTop = 8192.0f;
 
 // fp16 operands, fp32 accumulator, M = 128; N = 64 keys, and N = 128 coordinates with an MN-major B.
 constexpr uint32_t kIdescS = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
@@ -474,7 +476,7 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
         // the rows: finished, or a part of a cut segment. Their sums pass through shared memory (Q and K:
         // every product is done) from a thread a row to a warp a row
         if (n_rows > 0 && !dead) {
-            const float f = g.blind || sum == 0.0f ? 0.0f : __fmul_rn(__frcp_rn(sum), __fmul_rn(G, 1.0f / kVTop));
+            const float f = g.blind || sum == 0.0f ? 0.0f : __fmul_rn(__frcp_rn(sum), __fmul_rn(G, 1.0f / kTop));
             unsigned char *const stage = base + C::kOffQ + warp * 16384;
             if (!g.blind) {
 #pragma unroll 1
@@ -623,10 +625,10 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
                         G = up;
                     }
                 }
-                factor = __fmul_rn(factor, __fmul_rn(kVTop, __uint_as_float((254u << 23) - __float_as_uint(G))));
+                factor = __fmul_rn(factor, __fmul_rn(kTop, __uint_as_float((254u << 23) - __float_as_uint(G))));
             } else {
                 const float2 other = *reinterpret_cast<const float2 *>(base + C::kOffFac + (i % kRecStages) * kTileKeys * 8 + key * 8);
-                factor = __fmul_rn(factor, __fmul_rn(kKTop, __uint_as_float((254u << 23) - __float_as_uint(up))));
+                factor = __fmul_rn(factor, __fmul_rn(kTop, __uint_as_float((254u << 23) - __float_as_uint(up))));
                 if (!(fabsf(__fmul_rn(other.x, other.y)) < INFINITY)) factor = __uint_as_float(0x7fffffffu);
             }
             if (n >= KS && !warp_wait(&free[st], (use - 1) & 1u)) {
@@ -637,7 +639,7 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
                 Tile &t = sh.tile[st];
                 if (values) t.valid[warp & 3] = valid;
                 if (warp == 12) t.ratio = ratio, t.G = G;
-                if (warp == 8) sh.unit[n & 3] = __fmul_rn(up, 1.0f / kKTop);
+                if (warp == 8) sh.unit[n & 3] = __fmul_rn(up, 1.0f / kTop);
             }
             expand<kWide>(ops + st * C::kParts * kOp, key, rec, factor);
             fence_proxy_async_smem();
