@@ -247,9 +247,12 @@ wq_status tq3_cache_read(const uint8_t *k_pool, const uint8_t *v_pool, int64_t n
  * result is rounded by up to 2^-8); where either is fp32 the operands are split in two, and they are within
  * 2^-17 softmax_scale |q| |k_j| and 2^-19. Added to these, for what is far shorter than its neighbours: 2^-34
  * softmax_scale |q| |k| to a logit and 2^-34 |v| to a result, k and v the longest that any token of the sequence's
- * chunk sees, and to each term 2^-31 |v_j| times the row's largest weight, or 2^-27 of its longest term. Sums are fp32, in an order that
- * depends on the lengths alone. Record norms and scales are taken to be what the encoders write: not
- * negative, and a value vector shorter than 2^-100 may count as one of that length.
+ * chunk sees, and to each term 2^-31 |v_j| times the row's largest weight, or 2^-27 of its longest term.
+ * Sums are fp32. Their order, and which kernels run, follow from the counts and types, the lengths of the whole
+ * batch, max_q and pages_per_seq * page_size, not from timing: the same call gives the same bits, but a
+ * sequence's may change with the batch that it is in, with max_q or with the width of the table. Record norms and
+ * scales are taken to be what the encoders write: not negative, and a value vector shorter than 2^-100 may count
+ * as one of that length.
  * Errors: WQ_ERR_SHAPE (counts, strides, window or sinks out of range, softmax_scale not finite,
  * workspace too small), WQ_ERR_DTYPE, WQ_ERR_NULL, WQ_ERR_ALIGN, WQ_ERR_CUDA. n_tokens == 0 or
  * batch == 0 enqueues nothing. */
