@@ -36,8 +36,10 @@
 // without). Loops are rolled where they can be: code that runs once a segment is fetched anew each time, and at
 // 170 KB the kernel took 1220 us.
 //
-// Every wait is bounded; one that runs out sets fault bit 7, ends its role, and the others run out after
-// it. In-flight products get a bounded chance to finish before the tensor memory is freed.
+// Every wait is bounded; one that runs out sets fault bit 7 and ends its role's part of the segment. The others
+// finish theirs or run out after it, and all leave together at the segment's end, before anything is written over
+// its operands. Whatever ends a CTA, the warps that issued products wait for them (again with a limit) before the
+// tensor memory is freed.
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math.h>
@@ -108,6 +110,7 @@ struct Shared {
     // whose S is complete, and a softmax warp may be a tile behind that
     float unit[4];
     uint32_t tmem;
+    uint32_t dead;  // a wait has run out
     uint32_t most[2][2][4];  // per tile (alternately), pool and decoding warp: the largest factor
     int64_t scratch[kThreads / 32 + 4];
     Walk<256, kThreads> walk256;
@@ -317,23 +320,28 @@ struct Segment {
     }
 };
 
-// Between segments: all roles have left this one, and thread 0 goes to the next.
+// Between segments: all roles have left this one, and thread 0 goes to the next. Whether there is one; none
+// follows a wait that ran out (`dead`, of any role).
 template <bool kWide>
-__device__ __forceinline__ void next_segment(const Args &a, Walk<Cfg<kWide>::R, kThreads> &w, bool advance) {
+__device__ __forceinline__ bool next_segment(const Args &a, Shared &sh, bool dead) {
+    Walk<Cfg<kWide>::R, kThreads> &w = walk_of<kWide>(sh);
+    if (dead) sh.dead = 1;
     tc_fence_before();
     __syncthreads();
-    if (advance) {
+    const bool over = sh.dead != 0;
+    if (threadIdx.x == 0 && !over) {
         if (w.tile == 0 && w.take() != w.segment())
             *reinterpret_cast<Cut *>(a.ws + (int64_t)blockIdx.x * kCutBytes) = w.cut_here();
         w.next(a);
     }
     __syncthreads();
     tc_fence_after();
+    return !over && !w.done();
 }
 
-// Warps 0 .. 4 NB - 1. Returns whether a wait ran out (as the other roles do).
+// Warps 0 .. 4 NB - 1.
 template <bool kWide>
-__device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned char *base, uint32_t tmem) {
+__device__ __forceinline__ void softmax_role(const Args &a, Shared &sh, unsigned char *base, uint32_t tmem) {
     using C = Cfg<kWide>;
     constexpr int KS = C::KS, R = C::R;
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
@@ -341,11 +349,10 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + blk * 128 + lanes, tO = tmem + C::kTmemO + blk * 128 + lanes,
                    tP = tmem + C::kTmemP + blk * 128 + lanes;
-    bool dead = false;
     uint32_t n_tile = 0, n_s = 0, n_out[2] = {};  // tiles; tiles of this warp's block; results of each block
     float sg[4];
     lane_signs(a, lane, sg);
-    while (!w.done()) {
+    for (bool more = !w.done(), dead = false; more; more = next_segment<kWide>(a, sh, dead)) {
         const Segment<kWide> g(a, w);
         const int wr = g.r0 + 32 * warp, n_rows = min(32, g.rows - wr);  // the warp's rows; may be none
         float down = 1.0f;  // of this lane's row: its power of two
@@ -387,7 +394,7 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
             if (lane == 0) mbar_arrive(&sh.q_ready);
         }
         float M = -FLT_MAX, sum = 0.0f, G = 1.0f;
-        if (blk < g.nb && !g.blind && !dead) {
+        if (blk < g.nb && !g.blind) {
             const int pos = lane < n_rows ? g.before + token_of(a, wr + lane) : -1;
             // positions of the warp's rows, for tiles that all of them see whole
             const int lo = g.before + token_of(a, min(wr, g.rows - 1)), hi = g.before + token_of(a, min(wr + 31, g.rows - 1));
@@ -524,9 +531,7 @@ __device__ __forceinline__ bool softmax_role(const Args &a, Shared &sh, unsigned
             }
         }
         n_tile += g.blind ? 0 : g.take;
-        next_segment<kWide>(a, w, tid == 0);
     }
-    return dead;
 }
 
 __device__ __forceinline__ void cp_async8(uint32_t dst, const uint8_t *src, uint32_t bytes) {
@@ -535,7 +540,7 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const uint8_t *src, uint
 
 // Warps 8 .. 11 decode the keys and 12 .. 15 the values: a thread a record.
 template <bool kWide>
-__device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned char *base) {
+__device__ __forceinline__ void decode_role(const Args &a, Shared &sh, unsigned char *base) {
     using C = Cfg<kWide>;
     constexpr int KS = C::KS, R = C::R;
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
@@ -544,9 +549,8 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
     unsigned char *const recs = base + C::kOffRec + (values ? kRecBytes : 0), *const ops = base + (values ? C::kOffV : C::kOffK);
     uint64_t *const full = values ? sh.full_v : sh.full_k, *const free = values ? sh.free_v : sh.free_k;
     const uint8_t *const pool = values ? a.pools.v : a.pools.k;
-    bool dead = false;
     uint32_t n_tile = 0;
-    while (!w.done()) {
+    for (bool more = !w.done(), dead = false; more; more = next_segment<kWide>(a, sh, dead)) {
         const Segment<kWide> g(a, w);
         const int take = g.blind ? 0 : g.take;
         // Two steps ahead of a tile its page entry is asked for, one step ahead its record. -1: no row
@@ -648,9 +652,7 @@ __device__ __forceinline__ bool decode_role(const Args &a, Shared &sh, unsigned 
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         n_tile += take;
-        next_segment<kWide>(a, w, false);
     }
-    return dead;
 }
 
 // The same value in every lane, so that the compiler keeps it in a uniform register: the tensor-core
@@ -662,23 +664,22 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Warps 16 .. 15 + NB, one per block of rows.
+// Warps 16 .. 15 + NB, one per block of rows. Returns whether the warp has issued products.
 template <bool kWide>
 __device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned char *base, uint32_t tmem_) {
     using C = Cfg<kWide>;
     constexpr int KS = C::KS, R = C::R, kPasses = kWide ? 3 : 1;
     constexpr uint32_t kBlockOp = C::kParts * kOp >> 4, kLo = kOp >> 4, kHalf = 64 * 128 >> 4;  // in units of a descriptor's address
     Walk<R, kThreads> &w = walk_of<kWide>(sh);
-    bool dead = false;
     uint32_t n_tile = 0, segs = 0, n_s = 0;  // n_s: tiles of the block
     const uint32_t blk = uniform(threadIdx.x / 32 - kIssueWarp);
     const uint32_t tmem = uniform(tmem_), at = uniform(smem_u32(base));
     const uint32_t q = k_desc(at + C::kOffQ) + blk * kBlockOp, k0 = k_desc(at + C::kOffK), v0 = mn_desc(at + C::kOffV);
     const uint32_t tS = tmem + blk * 128, tO = tmem + C::kTmemO + blk * 128, tP = tmem + C::kTmemP + blk * 128;
-    while (!w.done()) {
+    for (bool more = !w.done(), dead = false; more; more = next_segment<kWide>(a, sh, dead)) {
         const Segment<kWide> g(a, w);
         const uint32_t take = uniform(g.blind ? 0 : g.take), nb = uniform(g.nb), mine = blk < nb ? take : 0;
-        if (mine > 0 && !dead && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
+        if (mine > 0 && !warp_wait(&sh.q_ready, segs & 1u)) dead = true;
 #pragma unroll 1
         for (uint32_t step = 0; step < 2 * mine + 2 && mine > 0 && !dead; ++step) {
             // S of half `half` of tile i, behind the value product of that half of tile i - 1
@@ -730,9 +731,8 @@ __device__ __forceinline__ bool issue_role(const Args &a, Shared &sh, unsigned c
         n_s += mine;
         ++segs;
         n_tile += take;
-        next_segment<kWide>(a, w, false);
     }
-    return dead;
+    return n_s > 0;
 }
 
 template <bool kWide>
@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     extern __shared__ unsigned char smem_raw[];
     unsigned char *const base = tq3::tile_base(smem_raw);
     Shared &sh = *reinterpret_cast<Shared *>(base + C::kOffShared);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5;
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -760,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         mbar_init(&sh.q_ready, 4 * NB);
         mbar_init(&sh.drain[0], 1);
         mbar_init(&sh.drain[1], 1);
+        sh.dead = 0;
     }
     if (warp == kIssueWarp) tmem_alloc(&sh.tmem, 512);
     // No wait here: the rows kernel, launched before this one in the same call, lets it start only when all
@@ -779,30 +780,31 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
 
-    bool dead = false;
+    bool issued = false;
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         if (warp < 4 * C::NB)
-            dead = softmax_role<kWide>(a, sh, base, tmem);
+            softmax_role<kWide>(a, sh, base, tmem);
         else
-            while (!w.done()) next_segment<kWide>(a, w, false);
+            for (bool more = !w.done(); more;) more = next_segment<kWide>(a, sh, false);
     } else if (warp < 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsDecode));
-        dead = decode_role<kWide>(a, sh, base);
+        decode_role<kWide>(a, sh, base);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
         if (warp < kIssueWarp + NB)
-            dead = issue_role<kWide>(a, sh, base, tmem);
+            issued = issue_role<kWide>(a, sh, base, tmem);
         else
-            while (!w.done()) next_segment<kWide>(a, w, false);
+            for (bool more = !w.done(); more;) more = next_segment<kWide>(a, sh, false);
     }
     pdl_trigger();
     pdl_wait();  // the join behind this kernel also needs the rows kernel's results
-    // products still in flight after a wait ran out get a bounded chance to finish
-    if (warp >= kIssueWarp && dead && lane == 0) {
+    // by the thread that issued them, the products: all done where no wait ran out
+    if (issued && elect_one()) {
         mma_commit(&sh.drain[warp - kIssueWarp]);
-        mbar_wait_bounded(&sh.drain[warp - kIssueWarp], 0, kMaxPolls);
+        if (!mbar_wait_bounded(&sh.drain[warp - kIssueWarp], 0, kMaxPolls)) atomicOr(&g_fault, 128u);
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == kIssueWarp) {
