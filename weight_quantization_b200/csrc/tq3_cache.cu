@@ -29,7 +29,7 @@ namespace tq3_cache {
 
 using tq3::SignMask;
 
-constexpr int kTile = 32;      // tokens per tile = threads per CTA
+constexpr int kTile = 32;      // tokens per tile, a lane each
 // Both bodies are some 2500 instructions long, more than the instruction cache keeps for warps that are each
 // somewhere else in it. Append's 12 warps of an SM (what 168 registers a thread allow) are one CTA that meets
 // before each item and so shares its fetches: 32768 tokens x 8 heads take 113 us with a CTA a warp, 102 with

@@ -1,7 +1,7 @@
 // Attention of ragged chunks of new tokens over a batch's paged TQ3 cache (page "tq3_core.py": the
 // cache is what tq3_quantize compresses and tq3_dequantize restores), causal, optionally with a
 // sliding window and first tokens that stay visible. How the work is cut and joined is in
-// tq3_chunk.cuh; this file has the entry point, the join, and the kernel for few rows.
+// tq3_chunk.cuh; this file has the entry point and the kernel for few rows.
 //
 // With q~ = H (s . q), f_j = norm_j scale_j of key j and g_j that of value j (post = 128^-1/2):
 //     logit_ij = softmax_scale post f_j (q~_i . c[idx_j]),
@@ -9,7 +9,7 @@
 // so both products are over centroids alone: 8 values, looked up as pairs (6 bits) in a table that
 // every lane has a column of in shared memory (a bank of its own, so no conflict).
 //
-// The rows kernel: a warp takes 32 keys at a time and 8 rows (NT is 1) of one KV head.
+// The rows kernel: a warp takes 32 keys at a time and 8 rows of one KV head.
 // S^T = C_K q~^T and O^T += C_V^T w with m16n8k16: the looked-up pairs are the A operands as they are
 // (the 128 coordinates may be summed in any order, so a lane takes the coordinates whose bits it can
 // read as whole words), and no decoded key or value ever leaves the registers. In log2 units the
@@ -53,6 +53,7 @@ constexpr int kSub = kTileKeys / kWarps;  // keys of a warp's step
 constexpr int kPiece = 16;                // keys of an m16n8k16's rows; a copy within a page
 static_assert(kSub == 2 * kPiece, "two pieces a step, a lane per key");
 constexpr int kStages = 3;
+constexpr int kFewRows = 8;  // rows of a block; with more per KV head a sequence may go to the tensor-core kernel
 constexpr int kPieceBytes = kPiece * tq3_cache::kRec;
 constexpr int kStageBytes = 4 * kPieceBytes;  // a step's key records, then its value records
 constexpr float kLazy = 8.0f;   // M_i is raised past this margin (log2 units)
@@ -62,9 +63,9 @@ constexpr float kTiny = 0x1p-100f;  // least g_j: a zero vector weighs 2^-100 in
 __device__ unsigned int g_fault;
 
 // Shared memory of the rows kernel.
-template <int NT, bool kWide>
+template <bool kWide>
 struct Layout {
-    static constexpr int kRows = 8 * NT;
+    static constexpr int kRows = kFewRows;
     static constexpr int kTable = kWide ? 64 * 32 * 8 : 64 * 32 * 4;
     static constexpr int kQ = kRows * 136;  // halves, rows padded by 16 bytes
     // a warp's stages; between segments, its rows' sums (132 floats a row)
@@ -140,7 +141,7 @@ __device__ __forceinline__ uint32_t field(const uint32_t (&w)[N], int o) {
     return s > 26 ? __funnelshift_r(w[q], w[q + 1 < N ? q + 1 : q], s - 7) : w[q] >> (s - 7);
 }
 
-template <int NT, bool kWide>
+template <bool kWide>
 __device__ __forceinline__ void product(float (&d)[4], const Pair<kWide> &a0, const Pair<kWide> &a1,
                                         const Pair<kWide> &a2, const Pair<kWide> &a3, const uint32_t (&hi)[2],
                                         const uint32_t (&lo)[2]) {
@@ -260,9 +261,9 @@ struct Steps {
 };
 constexpr int kAhead = kStages - 1;  // steps requested beyond the one in use
 
-template <int NT, bool kWide>
-__global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kernel(const __grid_constant__ Args a) {
-    using L = Layout<NT, kWide>;
+template <bool kWide>
+__global__ void __launch_bounds__(kThreads, kWide ? 2 : 4) rows_kernel(const __grid_constant__ Args a) {
+    using L = Layout<kWide>;
     constexpr int R = L::kRows;
     // centroids times kGain: for one fp16 the gain at which all four magnitudes are nearest to fp16 numbers
     constexpr float kGain = kWide ? 16.0f : 1.6196665f;
@@ -346,40 +347,34 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
         // (2^12 with the key's factor and 2^-12 with the row's, so that the row's times S stays finite)
         const float coef = __fmul_rn(a.coef, 4096.0f / kGain);
         // lane (g, t): row g, coordinates 32 t .. 32 t + 31, as the B operands of eight products
-        uint32_t qh[NT][8][2], ql[NT][kWide ? 8 : 1][2];
-        int p[NT][2];  // of rows 2 t and 2 t + 1: positions, scales
-        float down[NT][2];
+        uint32_t qh[8][2], ql[kWide ? 8 : 1][2];
+        int p[2];  // of rows 2 t and 2 t + 1: positions, scales
+        float down[2];
+        const __half *const from = qs + g * 136 + 32 * t;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const __half *const from = qs + (8 * n + g) * 136 + 32 * t;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint2 x = *reinterpret_cast<const uint2 *>(from + 4 * j);
-                qh[n][j][0] = x.x, qh[n][j][1] = x.y;
-                if (kWide) {
-                    const uint2 y = *reinterpret_cast<const uint2 *>(from + L::kQ + 4 * j);
-                    ql[n][kWide ? j : 0][0] = y.x, ql[n][kWide ? j : 0][1] = y.y;
-                }
+        for (int j = 0; j < 8; ++j) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(from + 4 * j);
+            qh[j][0] = x.x, qh[j][1] = x.y;
+            if (kWide) {
+                const uint2 y = *reinterpret_cast<const uint2 *>(from + L::kQ + 4 * j);
+                ql[kWide ? j : 0][0] = y.x, ql[kWide ? j : 0][1] = y.y;
             }
+        }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = r0 + 8 * n + 2 * t + e;
-                p[n][e] = r < rows ? before + token_of(a, r) : -1;
-                down[n][e] = downs[8 * n + 2 * t + e];
-            }
+        for (int e = 0; e < 2; ++e) {
+            const int r = r0 + 2 * t + e;
+            p[e] = r < rows ? before + token_of(a, r) : -1;
+            down[e] = downs[2 * t + e];
         }
         // the first and the second three bytes of a lane's 48 bits in the two words that hold them
         const uint32_t first = (g & 1) ? 0x5432u : 0x3210u, second = (g & 1) ? 0x7765u : 0x6543u;
-        float acc[NT][8][4], M[NT][2], l[NT][2];
+        float acc[8][4], M[2], l[2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.0f;
-            M[n][0] = M[n][1] = -FLT_MAX;
-            l[n][0] = l[n][1] = 0.0f;
-        }
+            for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
+        M[0] = M[1] = -FLT_MAX;
+        l[0] = l[1] = 0.0f;
 
         while (steps.used != steps.issued) {
             steps.request(a, w, warp, lane, 1);
@@ -403,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
             }
             __syncwarp();
 
-            float S[2][NT][4], live[2][NT][4];
+            float S[2][4], live[2][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 // keys g and g + 8 of the piece: words 3 t .. 3 t + 2 of the indices
@@ -412,88 +407,73 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
                 for (int i = 0; i < 3; ++i)
                     ka[i] = rec[14 * (kPiece * x + g) + 3 * t + i], kb[i] = rec[14 * (kPiece * x + g + 8) + 3 * t + i];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) S[x][n][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) S[x][e] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const Pair<kWide> a0 = lookup<kWide>(table, column, field(ka, 12 * j)),
                                       a1 = lookup<kWide>(table, column, field(kb, 12 * j)),
                                       a2 = lookup<kWide>(table, column, field(ka, 12 * j + 6)),
                                       a3 = lookup<kWide>(table, column, field(kb, 12 * j + 6));
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) product<NT, kWide>(S[x][n], a0, a1, a2, a3, qh[n][j], ql[n][kWide ? j : 0]);
+                    product<kWide>(S[x], a0, a1, a2, a3, qh[j], ql[kWide ? j : 0]);
                 }
                 const float4 fa = factor[kPiece * x + g], fb = factor[kPiece * x + g + 8];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const float4 f = e == 0 ? fa : fb;
-                        float s0, s1;
-                        upk2(mul2(pk2(S[x][n][e], S[x][n][e + 1]), pk2(down[n][0], down[n][1])), s0, s1);
-                        S[x][n][e] = __fmaf_rn(s0, f.x, f.y);
-                        S[x][n][e + 1] = __fmaf_rn(s1, f.x, f.y);
-                        live[x][n][e] = live[x][n][e + 1] = f.z;
-                    }
+                for (int e = 0; e < 4; e += 2) {
+                    const float4 f = e == 0 ? fa : fb;
+                    float s0, s1;
+                    upk2(mul2(pk2(S[x][e], S[x][e + 1]), pk2(down[0], down[1])), s0, s1);
+                    S[x][e] = __fmaf_rn(s0, f.x, f.y);
+                    S[x][e + 1] = __fmaf_rn(s1, f.x, f.y);
+                    live[x][e] = live[x][e + 1] = f.z;
+                }
             }
             if (!(j0 + kSub <= p_lo + 1 && (a.window == 0 || j0 > p_hi - a.window || j0 + kSub <= a.sinks))) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = j0 + kPiece * x + g + 8 * (e >> 1), pos = p[n][e & 1];
-                            const bool on = j <= pos && (a.window == 0 || j > pos - a.window || j < a.sinks);
-                            if (!on) S[x][n][e] = -INFINITY, live[x][n][e] = 0.0f;
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = j0 + kPiece * x + g + 8 * (e >> 1), pos = p[e & 1];
+                        const bool on = j <= pos && (a.window == 0 || j > pos - a.window || j < a.sinks);
+                        if (!on) S[x][e] = -INFINITY, live[x][e] = 0.0f;
+                    }
             }
             bool raise = false;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int e = 0; e < 2; ++e) {
+                const float m = max3(fmaxf(S[0][e], S[0][e + 2]), S[1][e], S[1][e + 2]);
+                raise |= m > __fadd_rn(M[e], kLazy);
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+                float alpha[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float m = max3(fmaxf(S[0][n][e], S[0][n][e + 2]), S[1][n][e], S[1][n][e + 2]);
-                    raise |= m > __fadd_rn(M[n][e], kLazy);
+                    float m = max3(fmaxf(S[0][e], S[0][e + 2]), S[1][e], S[1][e + 2]);
+#pragma unroll
+                    for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    m = fmaxf(m, M[e]);
+                    alpha[e] = ex2(__fsub_rn(M[e], m));
+                    M[e] = m;
+                    l[e] = __fmul_rn(l[e], alpha[e]);
                 }
-            if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float alpha[2];
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float m = max3(fmaxf(S[0][n][e], S[0][n][e + 2]), S[1][n][e], S[1][n][e + 2]);
-#pragma unroll
-                        for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        m = fmaxf(m, M[n][e]);
-                        alpha[e] = ex2(__fsub_rn(M[n][e], m));
-                        M[n][e] = m;
-                        l[n][e] = __fmul_rn(l[n][e], alpha[e]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[n][i][e] = __fmul_rn(acc[n][i][e], alpha[e & 1]);
-                }
+                    for (int e = 0; e < 4; ++e) acc[i][e] = __fmul_rn(acc[i][e], alpha[e & 1]);
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                uint32_t ph[NT][2], pl[NT][2];
+                uint32_t ph[2], pl[2];
+                float w4[4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float w4[4];
+                for (int e = 0; e < 4; ++e) {
+                    w4[e] = ex2(__fsub_rn(S[x][e], __fsub_rn(M[e & 1], kLift)));
+                    l[e & 1] = __fmaf_rn(w4[e], live[x][e], l[e & 1]);
+                }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        w4[e] = ex2(__fsub_rn(S[x][n][e], __fsub_rn(M[n][e & 1], kLift)));
-                        l[n][e & 1] = __fmaf_rn(w4[e], live[x][n][e], l[n][e & 1]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t hi = pack_half2(w4[2 * i], w4[2 * i + 1]);
-                        ph[n][i] = transpose8x8(hi);
-                        pl[n][i] = kWide ? transpose8x8(residue_half2(w4[2 * i], w4[2 * i + 1], hi)) : 0u;
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t hi = pack_half2(w4[2 * i], w4[2 * i + 1]);
+                    ph[i] = transpose8x8(hi);
+                    pl[i] = kWide ? transpose8x8(residue_half2(w4[2 * i], w4[2 * i + 1], hi)) : 0u;
                 }
                 // values of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9: coordinates 16 g .. 16 g + 15, bits 48 g
                 // on, as two groups of 24 bits
@@ -519,8 +499,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
                                           a1 = lookup<kWide>(table, column, field(o0, 6 * c)),
                                           a2 = lookup<kWide>(table, column, field(e1, 6 * c)),
                                           a3 = lookup<kWide>(table, column, field(o1, 6 * c));
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) product<NT, kWide>(acc[n][4 * h + c], a0, a1, a2, a3, ph[n], pl[n]);
+                        product<kWide>(acc[4 * h + c], a0, a1, a2, a3, ph, pl);
                     }
                 }
             }
@@ -531,19 +510,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !kWide ? 4 : 2) rows_kern
         // join the warps: row r by warp r % kWarps. No copy is in flight, so a warp's sums lie where its
         // stages were
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int e = 0; e < 2; ++e) {
+            float x = l[e];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = l[n][e];
+            for (int o = 4; o <= 16; o <<= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
+            const int r = 2 * t + e;
+            if (g == 0) *reinterpret_cast<float2 *>(stat + 2 * (warp * R + r)) = make_float2(M[e], x);
+            float *const to = reinterpret_cast<float *>(stages) + r * 132 + 16 * g;
 #pragma unroll
-                for (int o = 4; o <= 16; o <<= 1) x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
-                const int r = 8 * n + 2 * t + e;
-                if (g == 0) *reinterpret_cast<float2 *>(stat + 2 * (warp * R + r)) = make_float2(M[n][e], x);
-                float *const to = reinterpret_cast<float *>(stages) + r * 132 + 16 * g;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<float2 *>(to + 2 * i) = make_float2(acc[n][i][e], acc[n][i][e + 2]);
-            }
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float2 *>(to + 2 * i) = make_float2(acc[i][e], acc[i][e + 2]);
+        }
         __syncthreads();
         const bool whole = w.tile == 0 && take == w.segment();
         float *const slot = slot_at<R>(a, gridDim.x, 2 * blockIdx.x + (w.tile == 0));
@@ -588,14 +565,13 @@ unsigned int read_and_clear_fault() {
 }
 
 constexpr int kParts = 4 * kSms;
-constexpr int kFewRows = 8;  // rows per KV head of a sequence that the rows kernel serves
-inline int64_t rows_workspace() { return (workspace_bytes<8>(kParts) + 15) & ~int64_t(15); }
+inline int64_t rows_workspace() { return (workspace_bytes<kFewRows>(kParts) + 15) & ~int64_t(15); }
 
-template <int NT, bool kWide>
+template <bool kWide>
 wq_status run_rows(const Args &a, cudaStream_t s) {
-    using L = Layout<NT, kWide>;
-    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(rows_kernel<NT, kWide>), L::kBytes)) return WQ_ERR_CUDA;
-    launch_pdl(rows_kernel<NT, kWide>, kParts, kThreads, L::kBytes, s, a);
+    using L = Layout<kWide>;
+    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(rows_kernel<kWide>), L::kBytes)) return WQ_ERR_CUDA;
+    launch_pdl(rows_kernel<kWide>, kParts, kThreads, L::kBytes, s, a);
     return launch_status();
 }
 
@@ -666,10 +642,10 @@ extern "C" wq_status tq3_attention_chunk(const void *q, int q_dtype, int64_t n_t
     const double tiles = (double)blocks * (double)kv_heads * (double)((a.max_keys + 127) / 128);
     const bool few = max_q <= tq3_chunk::kFewRows / group || tiles <= (wide ? 1 : 3) * tq3_chunk::kParts;
     if (!few) a.rows_to = tq3_chunk::kFewRows + 1;
-    const wq_status st = wide ? tq3_chunk::run_rows<1, true>(a, s) : tq3_chunk::run_rows<1, false>(a, s);
+    const wq_status st = wide ? tq3_chunk::run_rows<true>(a, s) : tq3_chunk::run_rows<false>(a, s);
     if (st != WQ_OK) return st;
     if (few) {
-        tq3_chunk::launch_join<8>(a, tq3_chunk::kParts, a, 0, s);
+        tq3_chunk::launch_join<tq3_chunk::kFewRows>(a, tq3_chunk::kParts, a, 0, s);
         return launch_status();
     }
     tq3_chunk::Args many = a;
