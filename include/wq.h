@@ -237,7 +237,7 @@ wq_status tq3_cache_read(const uint8_t *k_pool, const uint8_t *v_pool, int64_t n
  *   q_start, kv_len  device, (batch + 1) and batch x int32, 4-byte aligned, q_start ascending.
  *   max_q      how many new tokens a sequence has at most, to choose kernels and the workspace by (and so
  *              does pages_per_seq * page_size, where that leaves little work); a sequence with more is
- *              served all the same.
+ *              served all the same. A table no wider than the keys need, and the true max_q, are served faster.
  *   window     0: none. sinks: first keys that a window leaves visible.
  *   out        device, [n_tokens][q_heads][128] of out_dtype, 16-byte aligned.
  *   workspace  device, 16-byte aligned, tq3_attention_chunk_workspace(max_q, q_heads / kv_heads) bytes,
@@ -251,8 +251,8 @@ wq_status tq3_cache_read(const uint8_t *k_pool, const uint8_t *v_pool, int64_t n
  * Sums are fp32. Their order, and which kernels run, follow from the counts and types, the lengths of the whole
  * batch, max_q and pages_per_seq * page_size, not from timing: the same call gives the same bits, but a
  * sequence's may change with the batch that it is in, with max_q or with the width of the table. Record norms and
- * scales are taken to be what the encoders write: not negative, and a value vector shorter than 2^-100 may count
- * as one of that length.
+ * scales are taken to be what the encoders write: not negative, a value's norm * scale below 2^126; a value vector
+ * shorter than 2^-100 may count as one of that length.
  * Errors: WQ_ERR_SHAPE (counts, strides, window or sinks out of range, softmax_scale not finite,
  * workspace too small), WQ_ERR_DTYPE, WQ_ERR_NULL, WQ_ERR_ALIGN, WQ_ERR_CUDA. n_tokens == 0 or
  * batch == 0 enqueues nothing. */

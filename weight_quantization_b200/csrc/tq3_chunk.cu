@@ -23,9 +23,10 @@
 // afterwards. For fp32 queries or results every operand is split into fp16 hi + lo (2^-22) and a product
 // takes three passes, hi hi + hi lo + lo hi. Sums are fp32.
 //
-// Measured: one token of 8 sequences of 32768 keys, 8 KV heads x 4 rows, bf16: 97.6 us with the join, 2.4 TB/s
-// of records where a copy reaches 6.55. A step of 32 keys is 983 warp instructions, of which the 128 lookups
-// are 500; the issue slots are 67% busy, the ALU 61%, the shared-memory pipe 58%, the tensor cores 17%. Three
+// Measured: one token of 8 sequences of 32768 keys, 8 KV heads x 4 rows, bf16: 99 us with the join, 2.4 TB/s
+// of records where a copy reaches 6.55. A step of 32 keys is 988 warp instructions, of which the 128 lookups
+// are 500; the issue slots are 66% busy, the ALU 61%, the shared-memory pipe 57%, the tensor cores 17%. With fp32
+// on either side, 158 us: two CTAs an SM, three passes. Three
 // CTAs of more registers in place of four take as long; right shifts as high halves of multiplications, to
 // spare the ALU, 108 us; keys ordered so that no record read meets a bank twice, no change.
 #include <cuda_runtime.h>
@@ -636,8 +637,8 @@ extern "C" wq_status tq3_attention_chunk(const void *q, int q_dtype, int64_t n_t
     // needs some 25 us to set up, transform, join and drain, so it is left out where no sequence has more than
     // 8 rows, and where so little work is left (as far as the host knows: the tables' room stands for the
     // lengths) that the former has three steps a CTA at most, one for split operands. 8 x 4 heads, 32 tokens
-    // over 515 keys: 24 us against 35; 64 tokens: 32 against 37; 32 over 1500: 29 against 39; fp32, 3 x up to 37
-    // tokens over 1531 keys, 4 heads: 28 against 43.
+    // over 515 keys: 25 us against 34; 64 tokens: 33 against 37; 32 over 1500: 30 against 39; fp32, 3 x up to 37
+    // tokens over 1531 keys, 4 heads: 28 against 43 (the second figure is the call's with a table for 131072 keys).
     const int64_t blocks = (n_tokens * group + 7) / 8 + batch;
     const double tiles = (double)blocks * (double)kv_heads * (double)((a.max_keys + 127) / 128);
     const bool few = max_q <= tq3_chunk::kFewRows / group || tiles <= (wide ? 1 : 3) * tq3_chunk::kParts;

@@ -28,10 +28,12 @@
 // For fp32 queries or results the operands are split hi + lo, a product takes three passes (hi hi, hi lo,
 // lo hi), and 128 rows and one stage of operands fill the shared memory.
 //
-// Measured, with the join: 2048 tokens over 16384 keys, 8 KV heads x 4 rows a token, bf16: 606-658 us, 780-850
-// TFLOP/s, about half of what a library product reaches. A tile and 256 rows take some 4500 cycles, of which the
-// products need 2200 and the exponentials (MUFU) 2050; the softmax of a half tile takes 2500 to 3000, half of it
-// waits for tensor memory and barriers, with 60% of the issue slots busy. 256 rows a CTA because each decoded
+// Measured, with the join: 2048 tokens over 16384 keys, 8 KV heads x 4 rows a token, bf16: 594 us at 1965 MHz, 866
+// TFLOP/s, about half of what a library product reaches (642 us where the power cap holds 1815 MHz); with fp32 on
+// either side 2.04 ms. A tile and 256 rows more take some 4500 cycles (from 6144 to 16384 keys), 5200 with the
+// segments' set-ups and ends, of which the products need 2200 and the exponentials (MUFU) 2050; the softmax of a
+// half tile takes 2500 to 3000, half of it waits for tensor memory and barriers, with 62% of the issue slots busy.
+// 256 rows a CTA because each decoded
 // operand then serves two products; with halves of 64 keys a block's softmax and its products overlap (697 us
 // without). Loops are rolled where they can be: code that runs once a segment is fetched anew each time, and at
 // 170 KB the kernel took 1220 us.
