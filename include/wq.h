@@ -188,11 +188,12 @@ wq_status tq3_attention_paged(const void *q, int q_dtype, int64_t heads, int64_t
 /* tq3_cache_append -- tq3_quantize of the K and the V of new tokens, written to their slots: token t
  * of head h goes to place slots[t] % page_size of page slots[t] / page_size, in both pools.
  * norm = max(||x||, 1e-8), scale = max(max|y|, 1e-8), idx_i = #{j : B_j < y_i / scale} with
- * y = H (s . x) / (sqrt(128) norm). Precision: the indices are those of real arithmetic (a vector with
- * a coefficient near a boundary is decided in fp64), so they do not depend on the order of the sums;
- * tq3_encode and tq3_encode_exact may differ from them by one step where y_i / scale is within 1e-6 of
- * a boundary. Norms agree with their real values to within 1e-6 relative, scales to within 6e-6 (the
- * bound; about 1e-7 in practice). A norm beyond the fp32 range is stored as +inf, with every index 3, as the page's division by it gives.
+ * y = H (s . x) / (sqrt(128) norm). Precision: a vector with a coefficient near a boundary is decided in
+ * fp64, so the indices are those of real arithmetic unless one lies within 2^-45 ||x|| of it (fp64's own
+ * error); tq3_encode and tq3_encode_exact may differ from them by one step where y_i / scale is within 1e-6
+ * of a boundary. Norms agree with their real values to within 1e-6 relative, scales to within 6e-6 (the
+ * bound; about 1e-7 in practice). A norm beyond the fp32 range is stored as +inf, with every index 3, as the
+ * page's division by it gives.
  *   k, v       device, tokens x kv_heads rows of 128 elements of dtype, 16-byte aligned. Strides are in
  *              elements, not negative, and multiples of 16 bytes: a slice of a fused projection will do.
  *   slots      device, tokens x int64, 8-byte aligned. A negative slot skips the token (padding); a slot

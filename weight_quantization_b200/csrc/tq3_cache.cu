@@ -14,10 +14,12 @@
 // contributions to z_i are bounded by Cauchy-Schwarz; T >= |x|), T by as much, and the polynomial
 // moves a boundary by 3e-7: 1e-5 in u, 4.5e-5 in Q (|Q'| <= 4.4). A vector with a coefficient whose
 // Q lies that close to an integer is decided again by the whole warp in fp64, from the input: four
-// coefficients a lane, so the indices are those of real arithmetic, whatever the order of the sums.
-// About one vector in 100 of Gaussian data takes that path; where all do (each has a coefficient of exactly 0, as
-// constant and one-hot vectors have) 32768 tokens x 8 heads of bf16 take 494 us in place of 86. Vectors whose fp32 sum of squares leaves
-// [1.1e-16, 1e37] take it too (the floors, overflow of z); an all-zero vector does not need it.
+// coefficients a lane. The indices are then those of real arithmetic, unless z_i lies within fp64's error of
+// a boundary: 7 * 2^-53 * sqrt(128) |x| of its own, and nearly that of T's, 2^-45 |x| together.
+// About one vector in 100 of Gaussian data takes that path; where all do (each has a coefficient of
+// exactly 0, as constant vectors have) 32768 tokens x 8 heads of bf16 take 494 us in place of 86. Vectors
+// whose fp32 sum of squares leaves [1.1e-16, 1e37] take it too (the floors, overflow of z); an all-zero
+// vector does not need it.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
