@@ -252,7 +252,7 @@ wq_status tq3_cache_read(const uint8_t *k_pool, const uint8_t *v_pool, int64_t n
  * Sums are fp32. Their order, and which kernels run, follow from the counts and types, the lengths of the whole
  * batch, max_q and pages_per_seq * page_size, not from timing: the same call gives the same bits, but a
  * sequence's may change with the batch that it is in, with max_q or with the width of the table. Record norms and
- * scales are taken to be what the encoders write: not negative, a value's norm * scale below 2^126; a value vector
+ * scales are taken to be what the encoders write: not negative, a value's norm * scale below 2^120; a value vector
  * shorter than 2^-100 may count as one of that length.
  * Errors: WQ_ERR_SHAPE (counts, strides, window or sinks out of range, softmax_scale not finite,
  * workspace too small), WQ_ERR_DTYPE, WQ_ERR_NULL, WQ_ERR_ALIGN, WQ_ERR_CUDA. n_tokens == 0 or
