@@ -1,6 +1,5 @@
-"""Host check of how the tensor-core chunk attention (csrc/tq3_chunk_mma.cu) ends, on its source: a wait that
-runs out there cannot be made to happen without spoiling a GPU's results, so the GPU tests only run the path on
-which none does.
+"""Host check of how the tensor-core chunk attention (csrc/tq3_chunk_mma.cu) ends, on its source: no correct
+call makes one of its waits run out, so the GPU tests only run the path on which none does.
 
 Whichever role's wait ran out, products may be in flight: the warps that issued some have to wait for them
 before the tensor memory is freed, and no role may go on to the next segment, whose queries are written where
